@@ -417,6 +417,108 @@ nvfp4_status moe_expert_forward_noalloc(const void* x_bf16, int64_t T, int64_t H
                                         const float* gs_h, void* out_bf16,
                                         const nvfp4_moe_taps* taps, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Router gradient: from the routing weights to the logits.
+ * The weights of nvfp4_router_topk are w = softmax over the k chosen logits,
+ * so with dw the gradient of the weights
+ *   dlogits[t][e] = sum over j with topk_ids[t][j] == e of
+ *                   w[t][j] * (dw[t][j] - sum_i w[t][i] * dw[t][i]),
+ * 0 for experts that were not chosen (fp32).  Every element of dlogits is
+ * written.  Equal ids in one row add up in slot order; ids outside [0, E)
+ * match no element, though their w and dw stay in the inner sum.
+ * topk_ids int32, topk_w float, dw float [T][k]; dlogits float [T][E].
+ * Shapes: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64).  No workspace.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                                   int64_t T, int E, int k, float* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dispatch: BF16 token rows in expert order, and its gradient; the gradient
+ * of nvfp4_moe_combine.
+ * inv_perm and expert_offsets are those of nvfp4_moe_route (inv_perm is a
+ * permutation of [0, T*k)); n = expert_offsets[E]; a pair (t, j) is routed if
+ * inv_perm[t*k+j] < n.
+ *
+ * nvfp4_moe_dispatch: rows[inv_perm[t*k+j]] = x[t] for routed pairs; rows
+ *   n .. T*k-1 (pairs with an invalid expert id) are zero.
+ * nvfp4_moe_dispatch_bwd: dx[t] = bf16_rne( sum over routed j of
+ *   drows[inv_perm[t*k+j]] ), fp32 sum in slot order; rows >= n are not read.
+ * nvfp4_moe_combine_bwd, for out = combine(y, w):
+ *   dy[inv_perm[t*k+j]] = bf16_rne( w[t][j] * dout[t] ) for routed pairs;
+ *     rows n .. T*k-1 are zero;
+ *   dw[t][j] = sum_n dout[t][n] * y[inv_perm[t*k+j]][n] (fp32) for routed
+ *     pairs, else 0.  dw may be NULL: then y is not read and may be NULL.
+ * x, dx, dout BF16 [T][H]; rows, drows, y, dy BF16 [T*k][H];
+ * topk_w, dw float [T][k].  Outputs must not overlap inputs.  Every sum has a
+ * fixed order: equal inputs give equal bits.
+ * Shapes: T >= 0, 1 <= k <= 64, 1 <= E <= 4096, H >= 8, H % 8 == 0,
+ *   H < 2^24, T*k < 2^31.  No workspace.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_moe_dispatch(const void* x_bf16, const int32_t* inv_perm,
+                                const int32_t* expert_offsets, int64_t T, int k, int E, int64_t H,
+                                void* rows_bf16, void* stream);
+nvfp4_status nvfp4_moe_dispatch_bwd(const void* drows_bf16, const int32_t* inv_perm,
+                                    const int32_t* expert_offsets, int64_t T, int k, int E,
+                                    int64_t H, void* dx_bf16, void* stream);
+nvfp4_status nvfp4_moe_combine_bwd(const void* dout_bf16, const void* y_bf16,
+                                   const int32_t* inv_perm, const float* topk_w,
+                                   const int32_t* expert_offsets, int64_t T, int k, int E,
+                                   int64_t H, void* dy_bf16, float* dw, void* stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 with a scale for each block of 128: quantisers.
+ * An FP8 activation of R rows and C columns (C % 16 == 0) is codes
+ * uint8[R][C] (OCP E4M3, bias 7, max 448) and scales float[R][ceil(C/128)],
+ * one per 128 columns of a row; an FP8 weight [N][K] is codes uint8[N][K] and
+ * scales float[ceil(N/128)][ceil(K/128)], one per 128 x 128 block.  A value is
+ * code * scale.  With b = max(amax of the block, 2^-100), every step in fp32,
+ * round to nearest even:
+ *   scale = b / 448,  r = 448 / b,  code = E4M3(v * r).
+ *
+ * nvfp4_fp8_quantize: v = x[row][col], row r at x + r*ld_x elements.
+ * nvfp4_fp8_swiglu_quantize: x rows hold [gate | up], cols columns each;
+ *   v = gate / (1 + exp(-gate)) * up in fp32 (not rounded to BF16), q has cols
+ *   columns.  The step between the two products of an FP8 expert.
+ *   n_rows (nullable, device int32[1], e.g. expert_offsets + E): rows >=
+ *   n_rows[0] are neither read nor written.
+ * nvfp4_fp8_quantize_weight: groups matrices [N][K], contiguous.
+ * Shapes: rows, groups, N >= 0; 16 <= cols, K < 2^24, multiples of 16; ld_x
+ *   at least the row's width and a multiple of 8; fewer than 2^31 scales in
+ *   all.  x, w 16-byte aligned, q 8-byte.  No workspace.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_fp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld_x,
+                                const int32_t* n_rows, uint8_t* q, float* sf, void* stream);
+nvfp4_status nvfp4_fp8_swiglu_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld_x,
+                                       const int32_t* n_rows, uint8_t* q, float* sf, void* stream);
+nvfp4_status nvfp4_fp8_quantize_weight(const void* w_bf16, int64_t groups, int64_t N, int64_t K,
+                                       uint8_t* q, float* sf, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Expert-grouped (or dense) product of FP8 operands with block scales.
+ * Row d of the grouped operand is A row s = a_row_src[d] / a_row_div
+ * (a_row_src != NULL) or A row d.  For e in [0, E) and d in
+ * [off[e], off[e+1]), off = expert_offsets:
+ *   c[d][n] = bf16_rne( sum_b a_sf[s][b] * b_sf[e][n/128][b]
+ *                         * sum_{k in block b} a_q[s][k] * b_q[e][n][k] ),
+ * fp32 accumulation, blocks of 128 along K (the last may be shorter).
+ * expert_offsets == NULL (E must be 1): a dense product, rows 0 .. M-1.
+ * Rows d >= off[E] are not written.  Requires off[E] <= M.  An A row index
+ * outside [0, rows_a) reads as a row of zeros.
+ * a_q uint8 [rows_a][K], a_sf float [rows_a][ceil(K/128)] (nvfp4_fp8_quantize);
+ * b_q uint8 [E][N][K], b_sf float [E][ceil(N/128)][ceil(K/128)]
+ * (nvfp4_fp8_quantize_weight; row-major, no packing); c BF16 [M][N].
+ * The gradient with respect to A is the same product of the quantised output
+ * gradient with the transposed weights (nvfp4_weight_layout transposes).
+ * Shapes: M >= 0, 1 <= E <= 4096, N >= 1, 16 <= K < 2^22, K % 16 == 0,
+ *   N*K < 2^31; with a_row_src also rows_a*K < 2^31 and a_row_div >= 1,
+ *   without it rows_a >= M.  a_q, b_q 16-byte aligned.  No workspace.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64_t rows_a,
+                                    const int32_t* a_row_src, int a_row_div,
+                                    const int32_t* expert_offsets, int E, int64_t M, int64_t N,
+                                    int64_t K, const uint8_t* b_q, const float* b_sf, void* c_bf16,
+                                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

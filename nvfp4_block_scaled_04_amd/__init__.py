@@ -12,6 +12,8 @@ from .binding import (  # noqa: F401
     gemm_splitk_workspace_bytes, gemm_workspace_bytes,
     grouped_gemm, lib, moe_combine, moe_expert_forward, moe_route, mx_expert_weights, pack_weights,
     prepare_expert_weights, quantize, quantize_scatter, router_topk, to_mx, weight_layout,
+    fp8_grouped_gemm, fp8_quantize, fp8_quantize_weight, fp8_swiglu_quantize, moe_combine_bwd,
+    moe_dispatch, moe_dispatch_bwd, router_topk_bwd,
 )
 
 __version__ = "0.1.0"

@@ -57,7 +57,22 @@ SIGNATURES = {
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                    c_void_p]),
+    "nvfp4_router_topk_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p,
+                                      c_void_p]),
+    "nvfp4_moe_dispatch": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int64,
+                                   c_void_p, c_void_p]),
+    "nvfp4_moe_combine_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                      c_int, c_int, c_int64, c_void_p, c_void_p, c_void_p]),
+    "nvfp4_fp8_quantize": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                   c_void_p]),
+    "nvfp4_fp8_quantize_weight": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                          c_void_p]),
+    "nvfp4_fp8_grouped_gemm": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int,
+                                       c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                       c_void_p]),
 }
+SIGNATURES["nvfp4_moe_dispatch_bwd"] = SIGNATURES["nvfp4_moe_dispatch"]
+SIGNATURES["nvfp4_fp8_swiglu_quantize"] = SIGNATURES["nvfp4_fp8_quantize"]
 # the MX variants take the same arguments as their NVFP4 counterparts
 SIGNATURES["nvfp4_mx_grouped_gemm"] = SIGNATURES["nvfp4_grouped_gemm"]
 SIGNATURES["moe_expert_forward_mx"] = SIGNATURES["moe_expert_forward"]
@@ -490,3 +505,187 @@ def mx_expert_weights(w: ExpertWeights, keep_rowmajor=True):
     p1, p2 = pack_weights(q1, s1), pack_weights(q2, s2)
     rm = dict(w1_q=q1, w1_sf=s1, w2_q=q2, w2_sf=s2) if keep_rowmajor else None
     return ExpertWeights(p1, w.gs_w1, p2, w.gs_w2, rm, mx=True)
+
+
+# ------------------------------------------------------------------ gradients and FP8
+
+FP8 = torch.float8_e4m3fn      # codes of the FP8 entry points (OCP E4M3)
+
+
+def _call(name, tensors, *args):
+    """Call entry point `name` with `args` and the current stream of the device
+    that holds the tensors (all on one device), with that device current."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: all tensors must be on one device")
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st != 0:
+        raise Nvfp4Error(st, name)
+
+
+def _out(t, shape, dtype, device, name="out"):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _dev(t, dtype, name, shape)
+
+
+def _scale_blocks(n):
+    return (n + 127) // 128
+
+
+def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
+    """Gradient of router_topk's weights with respect to the logits: topk_ids
+    (T, k) int32, topk_w (T, k) float32 as router_topk returned them, dw (T, k)
+    float32 -> dlogits (T, E) float32 (zero for experts not chosen)."""
+    _dev(topk_ids, torch.int32, "topk_ids")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be 2-D")
+    T, k = topk_ids.shape
+    _dev(topk_w, torch.float32, "topk_w", (T, k))
+    _dev(dw, torch.float32, "dw", (T, k))
+    o = _out(out, (T, E), torch.float32, topk_ids.device)
+    _call("nvfp4_router_topk_bwd", (topk_ids, topk_w, dw, o), _ptr(topk_ids), _ptr(topk_w), _ptr(dw),
+          T, E, k, _ptr(o))
+    return o
+
+
+def moe_dispatch(x, inv_perm, offsets, k, out=None):
+    """x (T, H) bf16 -> rows (T*k, H) bf16 in expert order: row inv_perm[t*k+j]
+    is token t; rows from offsets[E] on (invalid expert ids) are zero."""
+    _dev(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    T, H = x.shape
+    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+    _dev(offsets, torch.int32, "offsets")
+    o = _out(out, (T * k, H), torch.bfloat16, x.device)
+    _call("nvfp4_moe_dispatch", (x, inv_perm, offsets, o), _ptr(x), _ptr(inv_perm), _ptr(offsets), T,
+          k, offsets.numel() - 1, H, _ptr(o))
+    return o
+
+
+def moe_dispatch_bwd(drows, inv_perm, offsets, k, out=None):
+    """Gradient of moe_dispatch: drows (T*k, H) bf16 -> dx (T, H) bf16, each
+    token's routed row gradients summed in fp32."""
+    _dev(drows, torch.bfloat16, "drows")
+    if drows.dim() != 2 or k < 1 or drows.shape[0] % k:
+        raise ValueError("drows must be 2-D with T*k rows")
+    T, H = drows.shape[0] // k, drows.shape[1]
+    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+    _dev(offsets, torch.int32, "offsets")
+    o = _out(out, (T, H), torch.bfloat16, drows.device)
+    _call("nvfp4_moe_dispatch_bwd", (drows, inv_perm, offsets, o), _ptr(drows), _ptr(inv_perm),
+          _ptr(offsets), T, k, offsets.numel() - 1, H, _ptr(o))
+    return o
+
+
+def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
+    """Gradient of moe_combine: dout (T, H) bf16, y (T*k, H) bf16 -> (dy (T*k, H)
+    bf16, dw (T, k) float32).  dy rows from offsets[E] on are zero, and so is dw
+    of pairs with an invalid expert id.  need_dw=False: dw is None and y (which
+    may be None) is not read.  out: (dy, dw) tensors to write."""
+    _dev(dout, torch.bfloat16, "dout")
+    _dev(topk_w, torch.float32, "topk_w")
+    if dout.dim() != 2 or topk_w.dim() != 2:
+        raise ValueError("dout and topk_w must be 2-D")
+    T, H = dout.shape
+    k = topk_w.shape[1]
+    _dev(topk_w, torch.float32, "topk_w", (T, k))
+    if need_dw:
+        _dev(y, torch.bfloat16, "y", (T * k, H))
+    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+    _dev(offsets, torch.int32, "offsets")
+    dy, dw = out if out is not None else (None, None)
+    dy = _out(dy, (T * k, H), torch.bfloat16, dout.device, "dy")
+    dw = _out(dw, (T, k), torch.float32, dout.device, "dw") if need_dw else None
+    _call("nvfp4_moe_combine_bwd", (dout, y if need_dw else None, inv_perm, topk_w, offsets, dy, dw),
+          _ptr(dout), _ptr(y) if need_dw else None, _ptr(inv_perm), _ptr(topk_w), _ptr(offsets), T, k,
+          offsets.numel() - 1, H, _ptr(dy), _ptr(dw))
+    return dy, dw
+
+
+def _fp8_rows(name, x, C, offsets, out):
+    R = x.shape[0]
+    dev = x.device
+    q, sf = out if out is not None else (None, None)
+    q = _out(q, (R, C), FP8, dev, "q")
+    sf = _out(sf, (R, _scale_blocks(C)), torch.float32, dev, "sf")
+    n_rows = None
+    if offsets is not None:
+        _dev(offsets, torch.int32, "offsets")
+        n_rows = offsets.data_ptr() + 4 * (offsets.numel() - 1)
+    ld = x.stride(0) if R > 1 else (x.shape[1] + 7) // 8 * 8   # a one-row tensor's row stride is arbitrary
+    _call(name, (x, q, sf, offsets), _ptr(x), R, C, ld, n_rows, _ptr(q), _ptr(sf))
+    return q, sf
+
+
+def fp8_quantize(x, offsets=None, out=None):
+    """x (R, C) bf16 -> FP8 codes q (R, C) float8_e4m3fn and one float32 scale
+    per 128 columns of a row, sf (R, ceil(C/128)).  x's rows may be spaced apart.
+    offsets (expert offsets): rows from offsets[-1] on are left as they were."""
+    _dev(x, torch.bfloat16, "x", rows=True)
+    return _fp8_rows("nvfp4_fp8_quantize", x, x.shape[1], offsets, out)
+
+
+def fp8_swiglu_quantize(x, offsets=None, out=None):
+    """x (R, 2I) bf16 holding [gate | up] -> silu(gate) * up as FP8: codes q
+    (R, I) and scales sf (R, ceil(I/128)), as fp8_quantize makes them."""
+    _dev(x, torch.bfloat16, "x", rows=True)
+    if x.shape[1] % 2:
+        raise ValueError("x must hold [gate | up]: an even number of columns")
+    return _fp8_rows("nvfp4_fp8_swiglu_quantize", x, x.shape[1] // 2, offsets, out)
+
+
+def fp8_quantize_weight(w, out=None):
+    """w (G, N, K) bf16 -> FP8 codes q (G, N, K) float8_e4m3fn and one float32
+    scale per 128 x 128 block, sf (G, ceil(N/128), ceil(K/128))."""
+    _dev(w, torch.bfloat16, "w")
+    if w.dim() != 3:
+        raise ValueError("w must be (groups, N, K)")
+    G, N, K = w.shape
+    q, sf = out if out is not None else (None, None)
+    q = _out(q, (G, N, K), FP8, w.device, "q")
+    sf = _out(sf, (G, _scale_blocks(N), _scale_blocks(K)), torch.float32, w.device, "sf")
+    _call("nvfp4_fp8_quantize_weight", (w, q, sf), _ptr(w), G, N, K, _ptr(q), _ptr(sf))
+    return q, sf
+
+
+def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_row_div=1, out=None):
+    """Expert-grouped product of FP8 operands -> c (M, N) bf16.
+
+    a (R, K) float8_e4m3fn, a_sf (R, ceil(K/128)) from fp8_quantize; b (E, N, K),
+    b_sf (E, ceil(N/128), ceil(K/128)) from fp8_quantize_weight.  Row d of expert
+    e (offsets[e] <= d < offsets[e+1]) is row a_row_src[d] // a_row_div of a, or
+    row d; rows from offsets[E] on are not written.  offsets None: a dense
+    product with one expert.  M: rows of c (default: the length of a_row_src, or
+    R)."""
+    _dev(a, FP8, "a")
+    _dev(b, FP8, "b")
+    if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[2]:
+        raise ValueError("a must be (R, K) and b (E, N, K)")
+    R, K = a.shape
+    E, N, _ = b.shape
+    kb = _scale_blocks(K)
+    _dev(a_sf, torch.float32, "a_sf", (R, kb))
+    _dev(b_sf, torch.float32, "b_sf", (E, _scale_blocks(N), kb))
+    if offsets is not None:
+        _dev(offsets, torch.int32, "offsets", (E + 1,))
+    rows = R
+    if a_row_src is not None:
+        _dev(a_row_src, torch.int32, "a_row_src")
+        rows = a_row_src.numel()
+    if M is None:
+        M = rows
+    elif M > rows:
+        raise ValueError(f"M = {M} is more than the {rows} rows of the operand")
+    c = _out(out, (M, N), torch.bfloat16, a.device)
+    _call("nvfp4_fp8_grouped_gemm", (a, a_sf, b, b_sf, offsets, a_row_src, c), _ptr(a), _ptr(a_sf), R,
+          _ptr(a_row_src), a_row_div, _ptr(offsets), E, M, N, K, _ptr(b), _ptr(b_sf), _ptr(c))
+    return c

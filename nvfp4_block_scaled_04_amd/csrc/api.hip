@@ -639,3 +639,185 @@ extern "C" nvfp4_status moe_expert_forward_noalloc(
   return forward_impl(0, x_bf16, T, H, I, E, k, topk_ids, topk_w, w1_q, w1_sf, gs_w1, w2_q, w2_sf,
                       gs_w2, gs_h, out_bf16, taps, ws, NVFP4_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+// ---------------------------------------------------------------- gradients and FP8
+namespace {
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+nvfp4_status check_rows(int64_t T, int k, int E, int64_t H) {
+  if (T < 0) return fail(NVFP4_ERR_SHAPE, "T must be >= 0");
+  if (k < 1 || k > 64) return fail(NVFP4_ERR_SHAPE, "k must be in [1, 64] (got %d)", k);
+  if (E < 1 || E > 4096) return fail(NVFP4_ERR_SHAPE, "E must be in [1, 4096] (got %d)", E);
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "T*k must be < 2^31");
+  if (H < 8 || H % 8 || H >= (int64_t(1) << 24))
+    return fail(NVFP4_ERR_SHAPE, "H must be a positive multiple of 8 below 2^24 (got %lld)", (long long)H);
+  return NVFP4_OK;
+}
+
+nvfp4_status fp8_rows_impl(bool swiglu, const char* what, const void* x, int64_t rows, int64_t cols,
+                           int64_t ld_x, const int32_t* n_rows, uint8_t* q, float* sf, void* stream) {
+  const int64_t width = swiglu ? 2 * cols : cols;
+  if (rows < 0) return fail(NVFP4_ERR_SHAPE, "rows must be >= 0");
+  if (cols < 16 || cols % 16 || cols >= (int64_t(1) << 24))
+    return fail(NVFP4_ERR_SHAPE, "cols must be a positive multiple of 16 below 2^24 (got %lld)", (long long)cols);
+  if (ld_x < width || ld_x % 8 || ld_x >= (int64_t(1) << 40))
+    return fail(NVFP4_ERR_SHAPE, "ld_x must be >= the row's width and a multiple of 8 (got %lld)", (long long)ld_x);
+  if (rows >= (int64_t(1) << 31) || rows * ((cols + 127) / 128) >= (int64_t(1) << 31))
+    return fail(NVFP4_ERR_SHAPE, "tensor too large (2^31 scales or more)");
+  if (rows == 0) return NVFP4_OK;
+  if (!x || !q || !sf) return fail(NVFP4_ERR_INVALID_ARG, "x, q and sf must be non-NULL");
+  if (!aligned(x, 16) || !aligned(q, 8) || !aligned(sf, 4) || (n_rows && !aligned(n_rows, 4)))
+    return fail(NVFP4_ERR_INVALID_ARG, "x must be 16-byte, q 8-byte, sf and n_rows 4-byte aligned");
+  nvfp4_status st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_fp8_rows(swiglu, x, rows, cols, ld_x, n_rows, q, sf,
+                                       static_cast<hipStream_t>(stream)), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                                   int64_t T, int E, int k, float* dlogits, void* stream) {
+  if (T < 0 || T >= (int64_t(1) << 32)) return fail(NVFP4_ERR_SHAPE, "T must be in [0, 2^32)");
+  if (E < 1 || E > nvfp4::kRouterMaxExperts)
+    return fail(NVFP4_ERR_SHAPE, "E must be in [1, %d] (got %d)", nvfp4::kRouterMaxExperts, E);
+  if (k < 1 || k > 64 || k > E) return fail(NVFP4_ERR_SHAPE, "k must be in [1, min(E, 64)] (got %d)", k);
+  if (T == 0) return NVFP4_OK;
+  if (!topk_ids || !topk_w || !dw || !dlogits)
+    return fail(NVFP4_ERR_INVALID_ARG, "topk_ids, topk_w, dw and dlogits must be non-NULL");
+  if (!aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(dw, 4) || !aligned(dlogits, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "topk_ids, topk_w, dw and dlogits must be 4-byte aligned");
+  if (overlap(dlogits, 4 * T * E, topk_ids, 4 * T * k) || overlap(dlogits, 4 * T * E, topk_w, 4 * T * k) ||
+      overlap(dlogits, 4 * T * E, dw, 4 * T * k))
+    return fail(NVFP4_ERR_INVALID_ARG, "dlogits must not overlap the inputs");
+  nvfp4_status st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_router_topk_bwd(topk_ids, topk_w, dw, T, E, k, dlogits,
+                                              static_cast<hipStream_t>(stream)),
+                "nvfp4_router_topk_bwd launch");
+}
+
+nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* inv_perm, const int32_t* off, int64_t T,
+                                int k, int E, int64_t H, void* rows, void* stream) {
+  nvfp4_status st = check_rows(T, k, E, H);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (!x || !inv_perm || !off || !rows)
+    return fail(NVFP4_ERR_INVALID_ARG, "x, inv_perm, expert_offsets and rows must be non-NULL");
+  if (!aligned(x, 16) || !aligned(rows, 16)) return fail(NVFP4_ERR_INVALID_ARG, "x and rows must be 16-byte aligned");
+  if (overlap(rows, 2 * T * k * H, x, 2 * T * H)) return fail(NVFP4_ERR_INVALID_ARG, "rows must not overlap x");
+  st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_dispatch(x, inv_perm, off, T, k, E, H, rows, static_cast<hipStream_t>(stream)),
+                "nvfp4_moe_dispatch launch");
+}
+
+nvfp4_status nvfp4_moe_dispatch_bwd(const void* drows, const int32_t* inv_perm, const int32_t* off,
+                                    int64_t T, int k, int E, int64_t H, void* dx, void* stream) {
+  nvfp4_status st = check_rows(T, k, E, H);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (!drows || !inv_perm || !off || !dx)
+    return fail(NVFP4_ERR_INVALID_ARG, "drows, inv_perm, expert_offsets and dx must be non-NULL");
+  if (!aligned(drows, 16) || !aligned(dx, 16)) return fail(NVFP4_ERR_INVALID_ARG, "drows and dx must be 16-byte aligned");
+  if (overlap(dx, 2 * T * H, drows, 2 * T * k * H)) return fail(NVFP4_ERR_INVALID_ARG, "dx must not overlap drows");
+  st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_dispatch_bwd(drows, inv_perm, off, T, k, E, H, dx, static_cast<hipStream_t>(stream)),
+                "nvfp4_moe_dispatch_bwd launch");
+}
+
+nvfp4_status nvfp4_moe_combine_bwd(const void* dout, const void* y, const int32_t* inv_perm,
+                                   const float* topk_w, const int32_t* off, int64_t T, int k, int E,
+                                   int64_t H, void* dy, float* dw, void* stream) {
+  nvfp4_status st = check_rows(T, k, E, H);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (!dout || !inv_perm || !topk_w || !off || !dy || (dw && !y))
+    return fail(NVFP4_ERR_INVALID_ARG, "dout, inv_perm, topk_w, expert_offsets, dy and (with dw) y must be non-NULL");
+  if (!aligned(dout, 16) || !aligned(dy, 16) || (dw && !aligned(y, 16)) || !aligned(dw, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "dout, y and dy must be 16-byte and dw 4-byte aligned");
+  const int64_t rows = 2 * T * k * H;
+  if (overlap(dy, rows, dout, 2 * T * H) || overlap(dy, rows, topk_w, 4 * T * k) ||
+      (dw && (overlap(dy, rows, y, rows) || overlap(dy, rows, dw, 4 * T * k) ||
+              overlap(dw, 4 * T * k, topk_w, 4 * T * k) || overlap(dw, 4 * T * k, dout, 2 * T * H) ||
+              overlap(dw, 4 * T * k, y, rows))))
+    return fail(NVFP4_ERR_INVALID_ARG, "dy and dw must not overlap the inputs or each other");
+  st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_combine_bwd(dout, y, inv_perm, topk_w, off, T, k, E, H, dy, dw,
+                                          static_cast<hipStream_t>(stream)),
+                "nvfp4_moe_combine_bwd launch");
+}
+
+nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                const int32_t* n_rows, uint8_t* q, float* sf, void* stream) {
+  return fp8_rows_impl(false, "nvfp4_fp8_quantize launch", x, rows, cols, ld_x, n_rows, q, sf, stream);
+}
+
+nvfp4_status nvfp4_fp8_swiglu_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                       const int32_t* n_rows, uint8_t* q, float* sf, void* stream) {
+  return fp8_rows_impl(true, "nvfp4_fp8_swiglu_quantize launch", x, rows, cols, ld_x, n_rows, q, sf, stream);
+}
+
+nvfp4_status nvfp4_fp8_quantize_weight(const void* w, int64_t groups, int64_t N, int64_t K, uint8_t* q,
+                                       float* sf, void* stream) {
+  if (groups < 0 || N < 0) return fail(NVFP4_ERR_SHAPE, "groups and N must be >= 0");
+  if (K < 16 || K % 16 || K >= (int64_t(1) << 24))
+    return fail(NVFP4_ERR_SHAPE, "K must be a positive multiple of 16 below 2^24 (got %lld)", (long long)K);
+  if (groups >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "groups and N must be < 2^31");
+  const int64_t per = (N + 127) / 128 * ((K + 127) / 128);
+  if (per >= (int64_t(1) << 31) || (per > 0 && groups * per >= (int64_t(1) << 31)))
+    return fail(NVFP4_ERR_SHAPE, "tensor too large (2^31 scales or more)");
+  if (groups == 0 || N == 0) return NVFP4_OK;
+  if (!w || !q || !sf) return fail(NVFP4_ERR_INVALID_ARG, "w, q and sf must be non-NULL");
+  if (!aligned(w, 16) || !aligned(q, 8) || !aligned(sf, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "w must be 16-byte, q 8-byte and sf 4-byte aligned");
+  nvfp4_status st = check_arch();
+  if (st != NVFP4_OK) return st;
+  return finish(nvfp4::launch_fp8_weight(w, groups, N, K, q, sf, static_cast<hipStream_t>(stream)),
+                "nvfp4_fp8_quantize_weight launch");
+}
+
+nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64_t rows_a,
+                                    const int32_t* a_row_src, int a_row_div,
+                                    const int32_t* expert_offsets, int E, int64_t M, int64_t N,
+                                    int64_t K, const uint8_t* b_q, const float* b_sf, void* c,
+                                    void* stream) {
+  if (E < 1 || E > 4096) return fail(NVFP4_ERR_SHAPE, "E must be in [1, 4096] (got %d)", E);
+  if (M < 0 || M >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "M must be in [0, 2^31)");
+  if (K < 16 || K % 16 || K >= (int64_t(1) << 22))
+    return fail(NVFP4_ERR_SHAPE, "K must be a positive multiple of 16 below 2^22 (got %lld)", (long long)K);
+  if (N < 1 || N >= (int64_t(1) << 31) || N * K >= (int64_t(1) << 31))
+    return fail(NVFP4_ERR_SHAPE, "N must be positive and an expert's weight (N*K) below 2^31 elements");
+  if (rows_a < 0 || rows_a >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "rows_a must be in [0, 2^31)");
+  if (a_row_src) {
+    if (a_row_div < 1) return fail(NVFP4_ERR_SHAPE, "a_row_div must be >= 1");
+    if (rows_a * K >= (int64_t(1) << 31))
+      return fail(NVFP4_ERR_SHAPE, "gathered A codes must be below 2 GiB (rows_a*K = %lld)", (long long)(rows_a * K));
+  } else if (rows_a < M) {
+    return fail(NVFP4_ERR_SHAPE, "rows_a must be >= M without a gather");
+  }
+  if (!expert_offsets && E != 1) return fail(NVFP4_ERR_INVALID_ARG, "expert_offsets may be NULL only with one expert");
+  if (M == 0) return NVFP4_OK;
+  // workgroups: at most M m tiles times N/64 n tiles
+  if (M * ((N + 63) / 64) >= (int64_t(1) << 34) || (M / 16 + E) * ((N + 63) / 64) >= (int64_t(1) << 31))
+    return fail(NVFP4_ERR_SHAPE, "too many tiles (M, N too large)");
+  if (!a_q || !a_sf || !b_q || !b_sf || !c) return fail(NVFP4_ERR_INVALID_ARG, "A, B, their scales and c must be non-NULL");
+  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_sf, 4) || !aligned(b_sf, 4) || !aligned(c, 2))
+    return fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte, scales 4-byte and c 2-byte aligned");
+  if ((a_row_src && !aligned(a_row_src, 4)) || (expert_offsets && !aligned(expert_offsets, 4)))
+    return fail(NVFP4_ERR_INVALID_ARG, "a_row_src and expert_offsets must be 4-byte aligned");
+  nvfp4_status st = check_arch();
+  if (st != NVFP4_OK) return st;
+  const nvfp4::Fp8GemmArgs a{a_q, a_sf, rows_a, a_row_src, a_row_div, expert_offsets, E, M, N, K, b_q, b_sf, c};
+  return finish(nvfp4::launch_fp8_gemm(a, static_cast<hipStream_t>(stream)), "nvfp4_fp8_grouped_gemm launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,187 @@
+// BF16 -> FP8 block quantisers (gfx950).
+//
+// FP8 here is OCP E4M3 with one fp32 scale per 128 columns of a row
+// (activations) or per 128 x 128 block (weights).  With b = max(amax of the
+// block, 2^-100), every step in fp32 rounded to nearest even:
+//   scale = b / 448,  r = 448 / b,  code = E4M3(x * r).
+// |x * r| <= 448 * (1 + 2^-23), which rounds to at most 448, so no clamp is
+// needed; the 2^-100 floor keeps r finite and gives an all-zero block codes 0
+// and a positive scale.  v_cvt_pk_fp8_f32 rounds to nearest, ties to even.
+//
+// All three are bound by HBM: rows read 2 and write 1 + 4/128 bytes per
+// element, SwiGLU reads 4, weights read 2 and write 1.  Sixteen lanes hold
+// one 128-column block, 16 bytes (8 BF16) each, so its maximum is four lane
+// exchanges and nothing is read twice.
+#include "internal.hpp"
+#include "device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr float kFp8Max = 448.0f;
+constexpr float kFp8Floor = 7.888609052210118e-31f;   // 2^-100
+constexpr int kQThreads = 256;
+constexpr int kQGroups = kQThreads / 16;              // blocks of 128 per pass of a workgroup
+constexpr int kQRows = 4;                             // rows a lane group handles (same columns)
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  return m;
+}
+
+// largest over the 16 lanes that hold one 128-column block
+__device__ __forceinline__ float max16(float m) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  return m;
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float r) {
+#pragma clang fp contract(off)
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * r, x[1] * r, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * r, x[5] * r, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * r, x[7] * r, hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// silu(g) * u with every step rounded (no contraction): the same bits as the
+// formula g / (1 + exp(-g)) * u written out in fp32
+__device__ __forceinline__ void swiglu8(const uint4& gv, const uint4& uv, float (&h)[8]) {
+#pragma clang fp contract(off)
+  float g[8], u[8];
+  unpack8(gv, g);
+  unpack8(uv, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = g[i] / (1.0f + expf(-g[i]));
+    h[i] = s * u[i];
+  }
+}
+
+// One lane group per (kQRows rows, 128-column block).  SWIGLU: x rows hold
+// [gate | up], each cols wide.
+template <bool SWIGLU>
+__global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int cols, int64_t ld_x, int kblocks,
+    const int32_t* __restrict__ n_rows, uint8_t* __restrict__ q, float* __restrict__ sf) {
+  if (n_rows) {
+    const int64_t n = n_rows[0];
+    rows = n < rows ? n : rows;
+  }
+  const uint32_t unit = blockIdx.x * kQGroups + (threadIdx.x >> 4);
+  const uint32_t chunk = unit / (uint32_t)kblocks;
+  const int kb = (int)(unit - chunk * (uint32_t)kblocks);
+  const int64_t row0 = (int64_t)chunk * kQRows;
+  const int l = threadIdx.x & 15;
+  const int col = kb * 128 + l * 8;
+  const bool in = col < cols;
+  uint4 a[kQRows], b[kQRows];
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i) {
+    a[i] = make_uint4(0, 0, 0, 0);
+    b[i] = make_uint4(0, 0, 0, 0);
+    if (in && row0 + i < rows) {
+      const uint16_t* src = x + (row0 + i) * ld_x + col;
+      a[i] = *reinterpret_cast<const uint4*>(src);
+      if constexpr (SWIGLU) b[i] = *reinterpret_cast<const uint4*>(src + cols);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i) {
+    float v[8];
+    if constexpr (SWIGLU) swiglu8(a[i], b[i], v);
+    else unpack8(a[i], v);
+    const float m = fmaxf(max16(amax8(v)), kFp8Floor);
+    if (row0 + i < rows) {
+      if (in) *reinterpret_cast<uint2*>(q + (row0 + i) * cols + col) = encode8(v, kFp8Max / m);
+      if (l == 0) sf[(row0 + i) * kblocks + kb] = m / kFp8Max;
+    }
+  }
+}
+
+// One workgroup per 128 x 128 block: 16 rows per pass, eight passes in registers.
+__global__ __launch_bounds__(kQThreads) void fp8_weight_kernel(
+    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks,
+    uint8_t* __restrict__ q, float* __restrict__ sf) {
+  const uint32_t unit = blockIdx.x;
+  const uint32_t t = unit / (uint32_t)kblocks;
+  const int kb = (int)(unit - t * (uint32_t)kblocks);
+  const uint32_t g = t / (uint32_t)nblocks;
+  const int nb = (int)(t - g * (uint32_t)nblocks);
+  const int l = threadIdx.x & 15, rr = threadIdx.x >> 4;
+  const int64_t col = kb * 128 + l * 8;
+  const int64_t r0 = (int64_t)nb * 128 + rr;
+  const int64_t base = (int64_t)g * rows * cols;
+  uint4 a[8];
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + 16 * i;
+    a[i] = make_uint4(0, 0, 0, 0);
+    if (col < cols && row < rows) a[i] = *reinterpret_cast<const uint4*>(w + base + row * cols + col);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    unpack8(a[i], v);
+    m = fmaxf(m, amax8(v));
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  __shared__ float part[kQThreads / 64];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  m = fmaxf(m, kFp8Floor);
+  const float r = kFp8Max / m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + 16 * i;
+    float v[8];
+    unpack8(a[i], v);
+    if (col < cols && row < rows) *reinterpret_cast<uint2*>(q + base + row * cols + col) = encode8(v, r);
+  }
+  if (threadIdx.x == 0) sf[unit] = m / kFp8Max;
+}
+
+}  // namespace
+
+hipError_t launch_fp8_rows(bool swiglu, const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                           const int32_t* n_rows, uint8_t* q, float* sf, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const int kblocks = (int)((cols + 127) / 128);
+  const int64_t units = (rows + kQRows - 1) / kQRows * kblocks;
+  const unsigned grid = (unsigned)((units + kQGroups - 1) / kQGroups);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  if (swiglu)
+    fp8_rows_kernel<true><<<grid, kQThreads, 0, stream>>>(xp, rows, (int)cols, ld_x, kblocks, n_rows, q, sf);
+  else
+    fp8_rows_kernel<false><<<grid, kQThreads, 0, stream>>>(xp, rows, (int)cols, ld_x, kblocks, n_rows, q, sf);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_weight(const void* w, int64_t groups, int64_t rows, int64_t cols, uint8_t* q,
+                             float* sf, hipStream_t stream) {
+  if (groups == 0 || rows == 0) return hipSuccess;
+  const int nblocks = (int)((rows + 127) / 128), kblocks = (int)((cols + 127) / 128);
+  const unsigned grid = (unsigned)(groups * nblocks * kblocks);
+  fp8_weight_kernel<<<grid, kQThreads, 0, stream>>>(static_cast<const uint16_t*>(w), rows, cols, nblocks,
+                                                    kblocks, q, sf);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -103,6 +103,42 @@ constexpr int kRouterMaxExperts = 1024;
 hipError_t launch_router_topk(const float* logits, int64_t T, int E, int k, int32_t* topk_ids,
                               float* topk_w, hipStream_t stream);
 
+hipError_t launch_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                                  int64_t T, int E, int k, float* dlogits, hipStream_t stream);
+
+// fp8.hip: E4M3 codes and fp32 block scales; rows: one scale per 128 columns
+// (x rows ld_x apart; swiglu: x holds [gate | up], cols columns each; n_rows:
+// nullable device row count), weight: one per 128 x 128 block
+hipError_t launch_fp8_rows(bool swiglu, const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                           const int32_t* n_rows, uint8_t* q, float* sf, hipStream_t stream);
+hipError_t launch_fp8_weight(const void* w, int64_t groups, int64_t rows, int64_t cols, uint8_t* q,
+                             float* sf, hipStream_t stream);
+
+// fp8_gemm.hip
+struct Fp8GemmArgs {
+  const uint8_t* a_q;
+  const float* a_sf;
+  int64_t rows_a;
+  const int32_t* a_row_src;   // nullable
+  int a_row_div;
+  const int32_t* offsets;     // nullable (E == 1): all M rows
+  int E;
+  int64_t M, N, K;
+  const uint8_t* b_q;
+  const float* b_sf;
+  void* c;
+};
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream);
+
+// dispatch.hip
+hipError_t launch_dispatch(const void* x, const int32_t* inv_perm, const int32_t* offsets, int64_t T,
+                           int k, int E, int64_t H, void* rows, hipStream_t stream);
+hipError_t launch_dispatch_bwd(const void* drows, const int32_t* inv_perm, const int32_t* offsets,
+                               int64_t T, int k, int E, int64_t H, void* dx, hipStream_t stream);
+hipError_t launch_combine_bwd(const void* dout, const void* y, const int32_t* inv_perm,
+                              const float* topk_w, const int32_t* offsets, int64_t T, int k, int E,
+                              int64_t H, void* dy, float* dw, hipStream_t stream);
+
 // combine.hip
 hipError_t launch_combine(const void* y, const int32_t* inv_perm, const float* topk_w,
                           const int32_t* offsets, int64_t T, int k, int E, int64_t H, void* out,

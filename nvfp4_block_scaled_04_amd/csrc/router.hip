@@ -78,7 +78,68 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const float* __restric
   }
 }
 
+// Gradient of the weights with respect to the logits: with w the softmax over
+// the k chosen logits, dlogits[t][ids[t][j]] += w_j (dw_j - sum_i w_i dw_i),
+// 0 for every other expert.  One wave per token: lane j forms term j, lane l
+// then builds dlogits for the four experts 256 i + 4 l .. + 3 in registers,
+// taking the terms in slot order (ids repeated in a row add up in that order;
+// ids outside [0, E) match no expert).  Bound by the 4 E bytes written per
+// token.  VEC: E % 4 == 0, 16-byte stores.
+template <bool VEC>
+__global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __restrict__ topk_ids,
+                                                              const float* __restrict__ topk_w,
+                                                              const float* __restrict__ dw,
+                                                              int64_t T, int E, int k,
+                                                              float* __restrict__ dlogits) {
+#pragma clang fp contract(off)   // else w * g would round differently lane by lane in the exchanges
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;                          // the whole wave
+  float w = 0.0f, g = 0.0f;
+  int id = -1;
+  if (lane < k) {
+    w = topk_w[t * k + lane];
+    g = dw[t * k + lane];
+    id = topk_ids[t * k + lane];
+  }
+  float mean = w * g;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) mean += __shfl_xor(mean, off);
+  const float term = w * (g - mean);
+  // every lane takes every pass: the terms are read from lanes that may hold
+  // no expert of this pass
+  for (int base = 0; base < E; base += 256) {
+    const int e0 = base + 4 * lane;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < k; ++j) {
+      const int e = __builtin_amdgcn_readlane(id, j);
+      const float d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(term), j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += e == e0 + i ? d : 0.0f;
+    }
+    if constexpr (VEC) {
+      if (e0 < E) *reinterpret_cast<float4*>(dlogits + t * E + e0) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < E) dlogits[t * E + e0 + i] = v[i];
+    }
+  }
+}
+
 }  // namespace
+
+hipError_t launch_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                                  int64_t T, int E, int k, float* dlogits, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const unsigned blocks = (unsigned)((T + 3) / 4);
+  // 16-byte stores where every row starts on a 16-byte boundary
+  if (E % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0)
+    router_topk_bwd_kernel<true><<<blocks, 256, 0, stream>>>(topk_ids, topk_w, dw, T, E, k, dlogits);
+  else
+    router_topk_bwd_kernel<false><<<blocks, 256, 0, stream>>>(topk_ids, topk_w, dw, T, E, k, dlogits);
+  return hipGetLastError();
+}
 
 hipError_t launch_router_topk(const float* logits, int64_t T, int E, int k, int32_t* topk_ids,
                               float* topk_w, hipStream_t stream) {
