@@ -59,16 +59,31 @@ struct RowTile {
   int64_t row0;
 };
 
-// The mt-th tile of BM rows in expert order; false if there are fewer.  Lane
-// l scans expert e0 + l, 64 experts at a time.
+// Tile i of the tiles of at most BM rows that `rows` rows from `first` on are
+// cut into.  The tiles take even shares of the 32-row blocks: 300 rows are
+// 160 and 140, not 288 and 12, whose second tile would stream the whole
+// weight tile for a twelfth of the work.
+template <int BM>
+__device__ __forceinline__ bool cut_tile(const Fp8Params& p, int first, int rows, int i, RowTile& t) {
+  constexpr int kUnit = BM % 32 ? BM : 32;
+  const int n = (rows + BM - 1) / BM;
+  const int units = (rows + kUnit - 1) / kUnit, per = units / n, more = units - per * n;
+  const int at = (per * i + (i < more ? i : more)) * kUnit, size = (per + (i < more ? 1 : 0)) * kUnit;
+  int left = rows - at < size ? rows - at : size;
+  t.row0 = (int64_t)first + at;
+  if (t.row0 + left > p.M) left = (int)(p.M - t.row0);
+  t.nrows = left;
+  return left > 0;
+}
+
+// The mt-th tile of at most BM rows in expert order; false if there are fewer.
+// Lane l scans expert e0 + l, 64 experts at a time.
 template <int BM>
 __device__ __forceinline__ bool row_tile(const Fp8Params& p, int mt, RowTile& t) {
   if (!p.offsets) {
     t.e = 0;
-    t.row0 = (int64_t)mt * BM;
-    const int64_t left = p.M - t.row0;
-    t.nrows = (int)(left < BM ? left : BM);
-    return left > 0;
+    if (mt >= (p.M + BM - 1) / BM) return false;
+    return cut_tile<BM>(p, 0, (int)p.M, mt, t);
   }
   const int lane = threadIdx.x & 63;
   int before = 0;
@@ -85,15 +100,10 @@ __device__ __forceinline__ bool row_tile(const Fp8Params& p, int mt, RowTile& t)
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (mt < before + total) {
       const int src = __ffsll((unsigned long long)__ballot(before + incl > mt)) - 1;
-      const int first = __builtin_amdgcn_readlane(lo, src) +
-                        (mt - before - (__builtin_amdgcn_readlane(incl, src) -
-                                        __builtin_amdgcn_readlane(tiles, src))) * BM;
-      int left = __builtin_amdgcn_readlane(hi, src) - first;
-      if ((int64_t)first + left > p.M) left = (int)(p.M - first);
+      const int i = mt - before - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(tiles, src));
+      const int first = __builtin_amdgcn_readlane(lo, src);
       t.e = e0 + src;
-      t.row0 = first;
-      t.nrows = left < BM ? left : BM;
-      return t.nrows > 0;
+      return cut_tile<BM>(p, first, __builtin_amdgcn_readlane(hi, src) - first, i, t);
     }
     before += total;
   }
@@ -243,18 +253,32 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
 
 // ------------------------------------------------------------ many rows
 //
-// 256 weight rows x up to 256 tokens per workgroup of eight waves (4 along N,
+// 256 weight rows x up to 288 tokens per workgroup of eight waves (4 along N,
 // 2 along the tokens); a wave holds 64 weight rows x 16*JV tokens, JV the
-// 32-token blocks that the tile's rows fill.  Stages of one K block go from
-// HBM straight to LDS, double-buffered; 16-byte chunk q of a row lies at place
-// q ^ ((row >> 1) & 7), so the sixteen rows of a fragment read spread over all
-// banks.
+// 32-token blocks that the tile's rows fill.  Operands go from HBM straight to
+// LDS, where 16-byte chunk q of a row lies at place q ^ ((row >> 1) & 7), so
+// the sixteen rows of a fragment read spread over all banks.
+//
+// A stage is one K block, in JV steps of one token block each.  Its weight
+// fragments are in registers before it starts, so its weight buffer is free
+// early, and its token buffer in two parts (T1: blocks 0..JH-1, T2: the rest)
+// as the steps pass them.  Two barriers a stage hand the parts over:
+//   steps 0 .. JH-2      loads of T2 of stage b + 1
+//   barrier B            T2 of this stage has landed; weights and T1 are read
+//   steps JH-1 .. JV-2   loads of the weights and T1 of stage b + 2
+//   barrier S            weights and T1 of stage b + 1 have landed; T2 is read
+//   step JV-1            the next stage's fragments replace this one's
+// so that two buffers keep a whole stage's loads (72 KB) in flight at every
+// wait, and the loads are spread over the stage instead of queueing at its
+// start.
 
 constexpr int kTlWaves = 8;
-constexpr int kTlN = 256, kTlM = 256;
-constexpr int kTlTok = kTlN * 128;                    // LDS offsets in a stage: tokens,
-constexpr int kTlSf = kTlTok + kTlM * 128;            // token scales
-constexpr int kTlStage = kTlSf + kTlWaves * 64 * 4;   // (the upper four waves' scales are zeros)
+constexpr int kTlN = 256, kTlM = 288;
+constexpr int kTlTokLoads = 5;                        // 64-row token loads of a stage (kTlM rounded up)
+constexpr int kTlWBytes = kTlN * 128, kTlTBytes = kTlTokLoads * 64 * 128;
+constexpr int kTlSfWaves = 6;                         // five waves' token scales, one place for the others' zeros
+constexpr int kTlSfBytes = kTlSfWaves * 1024;         // four K blocks of scales for 64 tokens per wave
+constexpr int kTlLds = 2 * (kTlWBytes + kTlTBytes + kTlSfBytes);
 constexpr int kTlEpiStride = 64 * 2 + 16;             // LDS bytes per staged token row
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -271,103 +295,196 @@ __device__ __forceinline__ void bare_barrier() {
 
 struct TlLoads {
   __amdgpu_buffer_rsrc_t ra, rs, rb;
-  uint32_t wo[4], to[4], so;      // byte offsets of this lane's chunks and scale
+  uint32_t wo[4], to[kTlTokLoads], so;   // byte offsets of this lane's chunks and scales
   uint32_t cut;                   // kNowhere if the lane's chunk lies behind K in the last block
+  int KB, wave;
 };
 
-// Direct loads of K block b into `dst`; zeros for a block behind the last.  No
-// branch: code would move across it and out of the order the stage is written in.
-template <int JV>
-__device__ __forceinline__ void tl_issue(const TlLoads& L, int b, int KB, int wave, uint8_t* __restrict__ dst) {
-  const uint32_t cut = b < KB - 1 ? 0 : b == KB - 1 ? L.cut : kNowhere;
-  const int at = b < KB ? b * 128 : 0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rb, lds_addr(dst + (wave + 8 * c) * 1024), 16, L.wo[c] | cut, at, 0, 0);
-#pragma unroll
-  for (int c = 0; c < (JV + 1) / 2; ++c)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(L.ra, lds_addr(dst + kTlTok + (wave + 8 * c) * 1024), 16, L.to[c] | cut, at, 0, 0);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rs, lds_addr(dst + kTlSf + wave * 256), 4, L.so | (b < KB ? 0 : kNowhere), b < KB ? b * 4 : 0, 0, 0);
+// Direct loads of K block b, zeros for a block behind the last: 64 weight
+// rows c, 64 token rows c, the token scales of blocks b .. b + 3.  No branch:
+// code would move across it and out of the order the stages are written in.
+// POL: the weights' cache policy, 2 (non-temporal) where they are read once.
+__device__ __forceinline__ uint32_t tl_cut(const TlLoads& L, int b) {
+  return b < L.KB - 1 ? 0 : b == L.KB - 1 ? L.cut : kNowhere;
+}
+template <int POL>
+__device__ __forceinline__ void tl_load_w(const TlLoads& L, int b, int c, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rb, lds_addr(dst + (L.wave + 8 * c) * 1024), 16, L.wo[c] | tl_cut(L, b), b < L.KB ? b * 128 : 0, 0, POL);
+}
+__device__ __forceinline__ void tl_load_t(const TlLoads& L, int b, int c, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(L.ra, lds_addr(dst + (L.wave + 8 * c) * 1024), 16, L.to[c] | tl_cut(L, b), b < L.KB ? b * 128 : 0, 0, 0);
+}
+__device__ __forceinline__ void tl_load_s(const TlLoads& L, int b, uint8_t* dst) {
+  const int w = L.wave < kTlSfWaves ? L.wave : kTlSfWaves - 1;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rs, lds_addr(dst + w * 1024), 16, L.so | (b < L.KB ? 0 : kNowhere), b < L.KB ? b * 4 : 0, 0, 0);
 }
 
-__device__ __forceinline__ int8v tl_frag(const uint8_t* row, int at0, int at1) {
-  return join(*reinterpret_cast<const int4v*>(row + at0), *reinterpret_cast<const int4v*>(row + at1));
+template <int JV>
+struct TlState {
+  // 64-row loads: NT of the tokens, N1 of them in T1; JH = token blocks of T1
+  static constexpr int NT = (JV + 1) / 2, N1 = NT > 1 ? NT / 2 : 1, JH = 2 * N1;
+  static constexpr int kLoads = 4 + NT;
+  float4v acc[4][JV];
+  int8v w[4], t;                  // fragments of the next step
+  float s;                        // its scale
+  float4v dp[4];                  // products of the step before, not yet added
+  float sp;
+  int tok_at0, tok_at1, w_at0, w_at1, sf_at;   // this lane's LDS offsets
+};
+
+__device__ __forceinline__ int8v tl_frag(const uint8_t* base, int at0, int at1, int off) {
+  return join(*reinterpret_cast<const int4v*>(base + at0 + off), *reinterpret_cast<const int4v*>(base + at1 + off));
 }
 
-// One stage: the loads of block b + 1 into nxt, the products of block b from cur.
-template <int JV>
-__device__ __forceinline__ void tl_stage(float4v (&acc)[4][JV], const TlLoads& L, int b, int KB, int wave,
-                                         int lane, float sb, const uint8_t* __restrict__ cur,
-                                         uint8_t* __restrict__ nxt) {
-  const int r = lane & 15, g = lane >> 4, wn = wave >> 1, wt = wave & 1;
-  tl_issue<JV>(L, b + 1, KB, wave, nxt);
-  const int at0 = (g ^ ((r >> 1) & 7)) * 16, at1 = ((4 + g) ^ ((r >> 1) & 7)) * 16;
-  int8v w[4];
+#define NVFP4_TL_WAIT(n) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(n) : "memory")
+
+// The four products of the step's token block, and the scaling of the step
+// before, which needs no wait on the matrix unit.  J: its block; after the
+// last one's products the next stage's weight fragments are read from wn.
+template <int JV, int J>
+__device__ __forceinline__ void tl_products(TlState<JV>& st, const int8v& tn, float sn, const uint8_t* wn) {
+  constexpr int P = J > 0 ? J - 1 : JV - 1;
+  float4v d[4];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) w[f] = tl_frag(cur + (wn * 64 + 16 * f + r) * 128, at0, at1);
-  const uint8_t* tok = cur + kTlTok + (wt * 16 + r) * 128;
-  const uint8_t* sfs = cur + kTlSf + (wt * 16 + r) * 4;
-  int8v t = tl_frag(tok, at0, at1);
-  float s = *reinterpret_cast<const float*>(sfs) * sb;
-  float4v dp[4];                       // products of the block before, not yet added
-  float sp = 0.0f;
-  // Per token block: its four products, the next block's operands, and the
-  // scaling of the block before, which needs no wait on the matrix unit.
+  for (int f = 0; f < 4; ++f) {
+    d[f] = mfma_block(st.w[f], st.t);
+    if constexpr (J == JV - 1) st.w[f] = tl_frag(wn, st.w_at0, st.w_at1, f * 2048);
 #pragma unroll
-  for (int j = 0; j < JV; ++j) {
-    int8v tn = t;
-    float sn = 0.0f;
-    if (j + 1 < JV) {
-      tn = tl_frag(tok + (j + 1) * 4096, at0, at1);
-      sn = *reinterpret_cast<const float*>(sfs + (j + 1) * 128) * sb;
-    }
-    float4v d[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      d[f] = mfma_block(w[f], t);
-      if (j > 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][j - 1][i] = fmaf(dp[f][i], sp, acc[f][j - 1][i]);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < 4; ++f) dp[f] = d[f];
-    t = tn;
-    sp = s;
-    s = sn;
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < 4; ++i) st.acc[f][P][i] = fmaf(st.dp[f][i], st.sp, st.acc[f][P][i]);
+    asm volatile("" : "+v"(st.acc[f][P]));   // summed here: not sunk to a later block
   }
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[f][JV - 1][i] = fmaf(dp[f][i], sp, acc[f][JV - 1][i]);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  bare_barrier();
+  for (int f = 0; f < 4; ++f) st.dp[f] = d[f];
+  st.t = tn;
+  st.sp = st.s;
+  st.s = sn;
+  __builtin_amdgcn_sched_barrier(0);
 }
 
+// Steps 0 .. JH-2: fragments from T1 (t1), loads of T2 of block b + 1 into
+// nt2 and, every fourth stage, of the next four blocks' scales into ns.  The
+// pointers are __restrict__, and apart within one function: a fragment read
+// is then known not to alias the loads in flight, and gets no wait on them.
+template <int JV, int J>
+__device__ __forceinline__ void tl_first(TlState<JV>& st, const TlLoads& L, int b, float sb,
+                                         const uint8_t* __restrict__ t1, const uint8_t* __restrict__ sf,
+                                         uint8_t* __restrict__ nt) {
+  using S = TlState<JV>;
+  if constexpr (J < S::JH - 1) {
+    const int8v tn = tl_frag(t1, st.tok_at0, st.tok_at1, (J + 1) * 4096);
+    const float sn = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    constexpr int steps = S::JH - 1, n2 = S::NT - S::N1;
+#pragma unroll
+    for (int c = 0; c < n2; ++c)
+      if (c * steps / n2 == J) tl_load_t(L, b + 1, S::N1 + c, nt);
+    tl_products<JV, J>(st, tn, sn, nullptr);
+    tl_first<JV, J + 1>(st, L, b, sb, t1, sf, nt);
+  }
+}
+
+// Steps JH-1 .. JV-2: fragments from T2 (t2), loads of the weights and T1 of
+// block b + 2 into this stage's buffers.
+template <int JV, int J, int POL>
+__device__ __forceinline__ void tl_second(TlState<JV>& st, const TlLoads& L, int b, float sb,
+                                          const uint8_t* __restrict__ t2, const uint8_t* __restrict__ sf,
+                                          uint8_t* __restrict__ w, uint8_t* __restrict__ t1) {
+  using S = TlState<JV>;
+  if constexpr (J < JV - 1) {
+    const int8v tn = tl_frag(t2, st.tok_at0, st.tok_at1, (J + 1) * 4096);
+    const float sn = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    constexpr int steps = JV - S::JH, n = 4 + S::N1, at = J - (S::JH - 1);
+#pragma unroll
+    for (int c = 0; c < n; ++c)
+      if (c * steps / n == at) {
+        if (c < 4) tl_load_w<POL>(L, b + 2, c, w);
+        else tl_load_t(L, b + 2, c - 4, t1);
+      }
+    tl_products<JV, J>(st, tn, sn, nullptr);
+    tl_second<JV, J + 1, POL>(st, L, b, sb, t2, sf, w, t1);
+  }
+}
+
+// Step JV-1: the next stage's first fragments.
 template <int JV>
+__device__ __forceinline__ void tl_last(TlState<JV>& st, float sb_next, const uint8_t* __restrict__ wn,
+                                        const uint8_t* __restrict__ t1n, const uint8_t* __restrict__ sfn) {
+  const int8v tn = tl_frag(t1n, st.tok_at0, st.tok_at1, 0);
+  const float sn = *reinterpret_cast<const float*>(sfn + st.sf_at) * sb_next;
+  tl_products<JV, JV - 1>(st, tn, sn, wn);
+}
+
+template <int JV, int POL>
 __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int64_t n0, const TlLoads& L,
-                                       int wave, int lane, uint8_t* __restrict__ buf0, uint8_t* __restrict__ buf1) {
+                                       int lane, uint8_t* smem) {
+  using S = TlState<JV>;
+  const int wave = L.wave, KB = L.KB;
   const int r = lane & 15, g = lane >> 4, wn = wave >> 1, wt = wave & 1;
-  float4v acc[4][JV];
+  S st;
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < 4; ++f) {
+    st.dp[f] = float4v{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < JV; ++j) acc[f][j] = float4v{0, 0, 0, 0};
+    for (int j = 0; j < JV; ++j) st.acc[f][j] = float4v{0, 0, 0, 0};
+  }
+  st.sp = 0.0f;
+  const int at0 = (g ^ ((r >> 1) & 7)) * 16, at1 = ((4 + g) ^ ((r >> 1) & 7)) * 16;
+  st.w_at0 = (wn * 64 + r) * 128 + at0;
+  st.w_at1 = (wn * 64 + r) * 128 + at1;
+  st.tok_at0 = (wt * 16 + r) * 128 + at0;
+  st.tok_at1 = (wt * 16 + r) * 128 + at1;
+  st.sf_at = (wt * 16 + r) * 16;
   int nb = (int)((n0 + wn * 64) / 128);
   if (nb >= p.NB) nb = p.NB - 1;
   const float* bsf = p.b_sf + ((int64_t)t.e * p.NB + nb) * p.KB;
-  tl_issue<JV>(L, 0, p.KB, wave, buf0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  uint8_t *w0 = smem, *w1 = smem + kTlWBytes, *t0 = smem + 2 * kTlWBytes, *t1 = t0 + kTlTBytes, *sf = t1 + kTlTBytes;
+  auto sf_of = [&](int b) { return sf + ((b >> 2) & 1) * kTlSfBytes + (b & 3) * 4; };
+  // scale of block b's weights; 0 for the block of zeros behind an odd count
+  auto sb_of = [&](int b) { const float v = uniform_load(bsf, b < KB ? b : 0); return b < KB ? v : 0.0f; };
+
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tl_load_w<POL>(L, 0, c, w0);
+  tl_load_s(L, 0, sf);
+#pragma unroll
+  for (int c = 0; c < S::N1; ++c) tl_load_t(L, 0, c, t0);
+  asm volatile("" ::: "memory");   // these first: the wait below counts the later ones
+#pragma unroll
+  for (int c = S::N1; c < S::NT; ++c) tl_load_t(L, 0, c, t0);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tl_load_w<POL>(L, 1, c, w1);
+#pragma unroll
+  for (int c = 0; c < S::N1; ++c) tl_load_t(L, 1, c, t1);
+  NVFP4_TL_WAIT(S::kLoads);
   bare_barrier();
+#pragma unroll
+  for (int f = 0; f < 4; ++f) st.w[f] = tl_frag(w0, st.w_at0, st.w_at1, f * 2048);
+  st.t = tl_frag(t0, st.tok_at0, st.tok_at1, 0);
+  st.s = *reinterpret_cast<const float*>(sf + st.sf_at) * sb_of(0);
+
+  auto stage = [&](int b, uint8_t* wc, uint8_t* tc, uint8_t* wx, uint8_t* tx) {
+    const float sb = sb_of(b), sb_next = sb_of(b + 1);
+    if ((b & 3) == 0) tl_load_s(L, b + 4, sf + (((b >> 2) + 1) & 1) * kTlSfBytes);
+    tl_first<JV, 0>(st, L, b, sb, tc, sf_of(b), tx);
+    NVFP4_TL_WAIT(S::kLoads);
+    bare_barrier();
+    tl_second<JV, S::JH - 1, POL>(st, L, b, sb, tc, sf_of(b), wc, tc);
+    NVFP4_TL_WAIT(S::kLoads);
+    bare_barrier();
+    tl_last<JV>(st, sb_next, wx, tx, sf_of(b + 1));
+  };
   // an odd number of blocks runs one more of zeros
-  for (int b = 0; b < p.KB; b += 2) {
-    tl_stage<JV>(acc, L, b, p.KB, wave, lane, uniform_load(bsf, b), buf0, buf1);
-    tl_stage<JV>(acc, L, b + 1, p.KB, wave, lane, uniform_load(bsf, b + 1 < p.KB ? b + 1 : b), buf1, buf0);
+  for (int b = 0; b < KB; b += 2) {
+    stage(b, w0, t0, w1, t1);
+    stage(b + 1, w1, t1, w0, t0);
   }
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st.acc[f][JV - 1][i] = fmaf(st.dp[f][i], st.sp, st.acc[f][JV - 1][i]);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  bare_barrier();
   // BF16 through LDS (a region per wave): a lane holds four consecutive
   // columns of one token, the stores want sixteen bytes of a token's row
-  uint8_t* ep = buf0 + wave * (16 * kTlEpiStride);
+  uint8_t* ep = smem + wave * (16 * kTlEpiStride);
   const bool vec = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
   const int64_t nw = n0 + wn * 64;
 #pragma unroll
@@ -375,8 +492,8 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       uint2 o;
-      o.x = pack_bf16x2(acc[f][j][0], acc[f][j][1]);
-      o.y = pack_bf16x2(acc[f][j][2], acc[f][j][3]);
+      o.x = pack_bf16x2(st.acc[f][j][0], st.acc[f][j][1]);
+      o.y = pack_bf16x2(st.acc[f][j][2], st.acc[f][j][3]);
       *reinterpret_cast<uint2*>(ep + r * kTlEpiStride + 2 * (16 * f + 4 * g)) = o;
     }
 #pragma unroll
@@ -400,9 +517,13 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
   }
 }
 
+template <int POL>
 __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
+  // m tiles go round the XCDs (blocks do), so that the n tiles of one m tile
+  // share its tokens in one L2
+  const int xi = blockIdx.x >> 3, xm = xi / p.n_groups;
+  const int mt = xm * 8 + (blockIdx.x & 7), ng = xi - xm * p.n_groups;
   RowTile t;
   if (!row_tile<kTlM>(p, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
@@ -413,6 +534,8 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   const int64_t a_base = p.a_row_src ? 0 : t.row0;
   const int64_t a_rows = p.a_row_src ? p.rows_a : t.nrows;
   TlLoads L;
+  L.KB = p.KB;
+  L.wave = wave;
   L.ra = rsrc_of(p.a_q + a_base * K, a_rows * K);
   L.rs = rsrc_of(p.a_sf + a_base * p.KB, a_rows * p.KB * 4);
   L.rb = rsrc_of(p.b_q + (int64_t)t.e * p.N * K, p.N * K);
@@ -421,26 +544,28 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   L.cut = 16 * q < tail ? 0 : kNowhere;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int row = (wave + 8 * c) * 8 + (lane >> 3);
-    const int64_t n = n0 + row;
+    const int64_t n = n0 + (wave + 8 * c) * 8 + (lane >> 3);
     L.wo[c] = n < p.N ? (uint32_t)(n * K) + 16 * q : kNowhere;
-    const int64_t ar = a_row(p, t, row);
+  }
+#pragma unroll
+  for (int c = 0; c < kTlTokLoads; ++c) {
+    const int64_t ar = a_row(p, t, (wave + 8 * c) * 8 + (lane >> 3));
     L.to[c] = ar >= 0 ? (uint32_t)((ar - a_base) * K) + 16 * q : kNowhere;
   }
   {
-    const int64_t ar = wave < 4 ? a_row(p, t, wave * 64 + lane) : -1;
+    const int64_t ar = wave < kTlTokLoads ? a_row(p, t, wave * 64 + lane) : -1;
     L.so = ar >= 0 ? (uint32_t)((ar - a_base) * p.KB * 4) : kNowhere;
   }
-  uint8_t *b0 = smem, *b1 = smem + kTlStage;
   switch ((t.nrows + 31) / 32) {
-    case 1: tl_run<1>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 2: tl_run<2>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 3: tl_run<3>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 4: tl_run<4>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 5: tl_run<5>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 6: tl_run<6>(p, t, n0, L, wave, lane, b0, b1); break;
-    case 7: tl_run<7>(p, t, n0, L, wave, lane, b0, b1); break;
-    default: tl_run<8>(p, t, n0, L, wave, lane, b0, b1); break;
+    case 1:
+    case 2:
+    case 3: tl_run<3, POL>(p, t, n0, L, lane, smem); break;
+    case 4: tl_run<4, POL>(p, t, n0, L, lane, smem); break;
+    case 5: tl_run<5, POL>(p, t, n0, L, lane, smem); break;
+    case 6: tl_run<6, POL>(p, t, n0, L, lane, smem); break;
+    case 7: tl_run<7, POL>(p, t, n0, L, lane, smem); break;
+    case 8: tl_run<8, POL>(p, t, n0, L, lane, smem); break;
+    default: tl_run<9, POL>(p, t, n0, L, lane, smem); break;
   }
 }
 
@@ -462,9 +587,10 @@ hipError_t launch_skinny(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) 
 
 constexpr int kMaxDevices = 64;
 
+template <int POL>
 hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   p.n_groups = (int)((a.N + kTlN - 1) / kTlN);
-  const int64_t grid = tile_bound(a, kTlM) * p.n_groups;
+  const int64_t grid = (tile_bound(a, kTlM) + 7) / 8 * 8 * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -472,12 +598,12 @@ hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
   static std::atomic<bool> attr_set[kMaxDevices];
   if (!attr_set[dev].load(std::memory_order_relaxed)) {
-    err = hipFuncSetAttribute(reinterpret_cast<const void*>(fp8_tile_kernel),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, 2 * kTlStage);
+    err = hipFuncSetAttribute(reinterpret_cast<const void*>(fp8_tile_kernel<POL>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kTlLds);
     if (err != hipSuccess) return err;
     attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  fp8_tile_kernel<<<(unsigned)grid, kTlWaves * 64, 2 * kTlStage, stream>>>(p);
+  fp8_tile_kernel<POL><<<(unsigned)grid, kTlWaves * 64, kTlLds, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -493,7 +619,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   if (a.M <= 16 * (int64_t)a.E) return launch_skinny<1>(a, p, stream);
   if (a.M <= 32 * (int64_t)a.E) return launch_skinny<2>(a, p, stream);
   if (a.M <= 64 * (int64_t)a.E) return launch_skinny<4>(a, p, stream);
-  return launch_tile(a, p, stream);
+  return a.M <= kTlM * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
 }
 
 }  // namespace nvfp4
