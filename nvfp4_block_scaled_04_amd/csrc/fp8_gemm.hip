@@ -358,6 +358,16 @@ __device__ __forceinline__ void tl_products(TlState<JV>& st, const int8v& tn, fl
   st.t = tn;
   st.sp = st.s;
   st.s = sn;
+  __builtin_amdgcn_sched_group_barrier(2, 4, 0);
+  __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+  __builtin_amdgcn_sched_group_barrier(2, 4, 0);
+  __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+  __builtin_amdgcn_sched_group_barrier(256, 3, 0);
+  __builtin_amdgcn_sched_group_barrier(2, 4, 0);
+  __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+  __builtin_amdgcn_sched_group_barrier(2, 4, 0);
+  __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+  __builtin_amdgcn_sched_group_barrier(32, 1, 0);
   __builtin_amdgcn_sched_barrier(0);
 }
 
