@@ -35,7 +35,8 @@ struct Fp8Params {
   const uint8_t* b_q;
   const float* b_sf;
   uint16_t* c;
-  int n_groups;
+  int n_groups;               // n tiles
+  int bm;                     // rows of an m tile at most (tile kernel)
 };
 
 // A byte offset with this bit set lies behind every resource below (they all
@@ -59,16 +60,15 @@ struct RowTile {
   int64_t row0;
 };
 
-// Tile i of the tiles of at most BM rows that `rows` rows from `first` on are
+// Tile i of the tiles of at most bm rows that `rows` rows from `first` on are
 // cut into.  The tiles take even shares of the 32-row blocks: 300 rows are
 // 160 and 140, not 288 and 12, whose second tile would stream the whole
 // weight tile for a twelfth of the work.
-template <int BM>
-__device__ __forceinline__ bool cut_tile(const Fp8Params& p, int first, int rows, int i, RowTile& t) {
-  constexpr int kUnit = BM % 32 ? BM : 32;
-  const int n = (rows + BM - 1) / BM;
-  const int units = (rows + kUnit - 1) / kUnit, per = units / n, more = units - per * n;
-  const int at = (per * i + (i < more ? i : more)) * kUnit, size = (per + (i < more ? 1 : 0)) * kUnit;
+__device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, int rows, int i, RowTile& t) {
+  const int unit = bm % 32 ? bm : 32;
+  const int n = (rows + bm - 1) / bm;
+  const int units = (rows + unit - 1) / unit, per = units / n, more = units - per * n;
+  const int at = (per * i + (i < more ? i : more)) * unit, size = (per + (i < more ? 1 : 0)) * unit;
   int left = rows - at < size ? rows - at : size;
   t.row0 = (int64_t)first + at;
   if (t.row0 + left > p.M) left = (int)(p.M - t.row0);
@@ -76,21 +76,20 @@ __device__ __forceinline__ bool cut_tile(const Fp8Params& p, int first, int rows
   return left > 0;
 }
 
-// The mt-th tile of at most BM rows in expert order; false if there are fewer.
+// The mt-th tile of at most bm rows in expert order; false if there are fewer.
 // Lane l scans expert e0 + l, 64 experts at a time.
-template <int BM>
-__device__ __forceinline__ bool row_tile(const Fp8Params& p, int mt, RowTile& t) {
+__device__ __forceinline__ bool row_tile(const Fp8Params& p, int bm, int mt, RowTile& t) {
   if (!p.offsets) {
     t.e = 0;
-    if (mt >= (p.M + BM - 1) / BM) return false;
-    return cut_tile<BM>(p, 0, (int)p.M, mt, t);
+    if (mt >= (p.M + bm - 1) / bm) return false;
+    return cut_tile(p, bm, 0, (int)p.M, mt, t);
   }
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     const int e = e0 + lane;
     const int lo = p.offsets[e < p.E ? e : p.E], hi = p.offsets[e < p.E ? e + 1 : p.E];
-    const int tiles = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    const int tiles = hi > lo ? (hi - lo + bm - 1) / bm : 0;
     int incl = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -103,7 +102,7 @@ __device__ __forceinline__ bool row_tile(const Fp8Params& p, int mt, RowTile& t)
       const int i = mt - before - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(tiles, src));
       const int first = __builtin_amdgcn_readlane(lo, src);
       t.e = e0 + src;
-      return cut_tile<BM>(p, first, __builtin_amdgcn_readlane(hi, src) - first, i, t);
+      return cut_tile(p, bm, first, __builtin_amdgcn_readlane(hi, src) - first, i, t);
     }
     before += total;
   }
@@ -124,18 +123,18 @@ __device__ __forceinline__ float4v mfma_block(const int8v& w, const int8v& t) {
 
 // ------------------------------------------------------------ few rows
 //
-// 64 weight rows x up to 16*JT tokens per workgroup.  Weights are read once
-// and by one wave only, so they go straight to registers; the eight waves
-// split the K blocks (block b to wave b % 8, so the workgroup reads 1 KiB
-// runs of each weight row) and join through LDS in wave order.
+// 16*RF weight rows x up to 16*JT tokens per workgroup, for products whose
+// tiles would leave most CUs idle.  Weights go straight to registers; the
+// eight waves split the K blocks (block b to wave b % 8, so the workgroup reads
+// 1 KiB runs of each weight row), D blocks in flight per wave, and join
+// through LDS in wave order.  Bound by latency: the fewer rows, the more
+// workgroups pull at once.
 
 constexpr int kSkWaves = 8;
-constexpr int kSkRows = 64;
-constexpr int kSkStride = kSkRows + 4;      // LDS floats per token
 
-template <int JT>
+template <int RF, int JT>
 struct SkFrag {
-  int8v w[4], t[JT];
+  int8v w[RF], t[JT];
   float s[JT], sb;
 };
 
@@ -143,15 +142,16 @@ __device__ __forceinline__ int8v join(const int4v& lo, const int4v& hi) {
   return int8v{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-template <int JT>
+template <int RF, int JT, int D>
 __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) {
-  __shared__ float red[kSkWaves][16][kSkStride];
+  constexpr int kRows = 16 * RF, kStride = kRows + 4;
+  __shared__ float red[kSkWaves][16][kStride];
   const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
   RowTile t;
-  if (!row_tile<16 * JT>(p, mt, t)) return;
+  if (!row_tile(p, 16 * JT, mt, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)ng * kSkRows;
+  const int64_t n0 = (int64_t)ng * kRows;
   const int64_t K = p.K;
 
   // without a gather the resource starts at the tile's first row, so offsets
@@ -163,9 +163,9 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
   const auto rb = rsrc_of(p.b_q + (int64_t)t.e * p.N * K, p.N * K);
   const float* bsf = p.b_sf + ((int64_t)t.e * p.NB + n0 / 128) * p.KB;
 
-  uint32_t wo[4], to[JT], so[JT];
+  uint32_t wo[RF], to[JT], so[JT];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
+  for (int f = 0; f < RF; ++f) {
     const int64_t n = n0 + 16 * f + r;
     wo[f] = n < p.N ? (uint32_t)(n * K) + 16 * g : kNowhere;
   }
@@ -179,18 +179,18 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
   const int tail = p.K - (p.KB - 1) * 128;
   const uint32_t cut_lo = 16 * g < tail ? 0 : kNowhere, cut_hi = 64 + 16 * g < tail ? 0 : kNowhere;
 
-  float4v acc[4][JT];
+  float4v acc[RF][JT];
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < RF; ++f)
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[f][j] = float4v{0, 0, 0, 0};
 
-  auto load = [&](int b, SkFrag<JT>& x) {
+  auto load = [&](int b, SkFrag<RF, JT>& x) {
     const bool none = b >= p.KB, last = b == p.KB - 1;
     const uint32_t lo = none ? kNowhere : last ? cut_lo : 0, hi = none ? kNowhere : last ? cut_hi : 0;
     const int at = none ? 0 : b * 128;
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < RF; ++f)
       x.w[f] = join(__builtin_amdgcn_raw_buffer_load_b128(rb, wo[f] | lo, at, 2),
                     __builtin_amdgcn_raw_buffer_load_b128(rb, (wo[f] + 64) | hi, at, 2));
 #pragma unroll
@@ -199,53 +199,58 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
                     __builtin_amdgcn_raw_buffer_load_b128(ra, (to[j] + 64) | hi, at, 0));
       x.s[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so[j] | (none ? kNowhere : 0), none ? 0 : b * 4, 0));
     }
-    x.sb = bsf[none ? 0 : b];
+    x.sb = uniform_load(bsf, none ? 0 : b);
+    asm volatile("" ::: "memory");      // issued here, not where they are used
   };
-  auto add = [&](const SkFrag<JT>& x) {
+  auto add = [&](const SkFrag<RF, JT>& x) {
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
       const float s = x.s[j] * x.sb;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < RF; ++f) {
         const float4v d = mfma_block(x.w[f], x.t[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[f][j][i] = fmaf(d[i], s, acc[f][j][i]);
       }
     }
   };
-  SkFrag<JT> x0, x1;
-  load(wave, x0);
-  for (int b = wave; b < p.KB; b += 2 * kSkWaves) {
-    load(b + kSkWaves, x1);
-    add(x0);
-    load(b + 2 * kSkWaves, x0);
-    add(x1);
+  SkFrag<RF, JT> x[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wave + kSkWaves * d, x[d]);
+  for (int b = wave; b < p.KB; b += D * kSkWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      add(x[d]);
+      load(b + kSkWaves * (d + D), x[d]);
+    }
   }
 
-  const int tok = threadIdx.x >> 5, n2 = (threadIdx.x & 31) * 2;
 #pragma unroll
   for (int j = 0; j < JT; ++j) {
     if (16 * j >= t.nrows) break;
     if (j) __syncthreads();
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < RF; ++f)
       *reinterpret_cast<float4v*>(&red[wave][r][16 * f + 4 * g]) = acc[f][j];
     __syncthreads();
-    float v0 = 0.0f, v1 = 0.0f;
+    for (int o = threadIdx.x; o < 16 * kRows / 2; o += kSkWaves * 64) {
+      const int tok = o / (kRows / 2), n2 = o % (kRows / 2) * 2;
+      float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSkWaves; ++w) {
-      const float2 v = *reinterpret_cast<const float2*>(&red[w][tok][n2]);
-      v0 += v.x;
-      v1 += v.y;
-    }
-    if (16 * j + tok < t.nrows && n0 + n2 < p.N) {
-      uint16_t* dst = p.c + (t.row0 + 16 * j + tok) * p.N + n0 + n2;
-      const uint32_t o = pack_bf16x2(v0, v1);
-      if (p.N % 2 == 0) {
-        *reinterpret_cast<uint32_t*>(dst) = o;
-      } else {
-        dst[0] = (uint16_t)o;
-        if (n0 + n2 + 1 < p.N) dst[1] = (uint16_t)(o >> 16);
+      for (int w = 0; w < kSkWaves; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(&red[w][tok][n2]);
+        v0 += v.x;
+        v1 += v.y;
+      }
+      if (16 * j + tok < t.nrows && n0 + n2 < p.N) {
+        uint16_t* dst = p.c + (t.row0 + 16 * j + tok) * p.N + n0 + n2;
+        const uint32_t q = pack_bf16x2(v0, v1);
+        if (p.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 3) == 0) {
+          *reinterpret_cast<uint32_t*>(dst) = q;
+        } else {
+          dst[0] = (uint16_t)q;
+          if (n0 + n2 + 1 < p.N) dst[1] = (uint16_t)(q >> 16);
+        }
       }
     }
   }
@@ -278,7 +283,7 @@ struct StTok {
 
 struct StLoads {
   __amdgpu_buffer_rsrc_t ra, rs, rb;
-  uint32_t wo[4], to[2], so[2];         // byte offsets of this lane's chunks and scales
+  uint32_t wo[4], to[4], so[4];         // byte offsets of this lane's chunks and scales
   uint32_t w_cut[2], t_cut_lo, t_cut_hi;   // kNowhere for chunks behind K in the last block (w: even, odd loads)
   int KB, at0, at1;                     // at0, at1: this lane's fragment chunks in a stage
 };
@@ -339,7 +344,7 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   __shared__ __align__(1024) uint8_t smem[kStWaves * kStRing * kStStage];
   const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
   RowTile t;
-  if (!row_tile<16 * JT>(p, mt, t)) return;
+  if (!row_tile(p, 16 * JT, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
   t.nrows = __builtin_amdgcn_readfirstlane(t.nrows);
   t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
@@ -445,7 +450,7 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
 // start.
 
 constexpr int kTlWaves = 8;
-constexpr int kTlN = 256, kTlM = 288;
+constexpr int kTlN = 256, kTlM = 288, kTlMin = 96;
 constexpr int kTlTokLoads = 5;                        // 64-row token loads of a stage (kTlM rounded up)
 constexpr int kTlWBytes = kTlN * 128, kTlTBytes = kTlTokLoads * 64 * 128;
 constexpr int kTlSfWaves = 6;                         // five waves' token scales, one place for the others' zeros
@@ -702,7 +707,7 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   const int xi = blockIdx.x >> 3, xm = xi / p.n_groups;
   const int mt = xm * 8 + (blockIdx.x & 7), ng = xi - xm * p.n_groups;
   RowTile t;
-  if (!row_tile<kTlM>(p, mt, t)) return;
+  if (!row_tile(p, p.bm, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
   t.nrows = __builtin_amdgcn_readfirstlane(t.nrows);
   t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
@@ -762,12 +767,12 @@ hipError_t launch_stream(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) 
   return hipGetLastError();
 }
 
-template <int JT>
+template <int RF, int JT, int D>
 hipError_t launch_skinny(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
-  p.n_groups = (int)((a.N + kSkRows - 1) / kSkRows);
+  p.n_groups = (int)((a.N + 16 * RF - 1) / (16 * RF));
   const int64_t grid = tile_bound(a, 16 * JT) * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  fp8_skinny_kernel<JT><<<(unsigned)grid, kSkWaves * 64, 0, stream>>>(p);
+  fp8_skinny_kernel<RF, JT, D><<<(unsigned)grid, kSkWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -776,7 +781,7 @@ constexpr int kMaxDevices = 64;
 template <int POL>
 hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   p.n_groups = (int)((a.N + kTlN - 1) / kTlN);
-  const int64_t grid = (tile_bound(a, kTlM) + 7) / 8 * 8 * p.n_groups;
+  const int64_t grid = (tile_bound(a, p.bm) + 7) / 8 * 8 * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -793,6 +798,66 @@ hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+std::atomic<int> g_cus[kMaxDevices];
+
+hipError_t device_cus(int& cus) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+  cus = g_cus[dev].load(std::memory_order_relaxed);
+  if (cus > 0) return hipSuccess;
+  err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (err != hipSuccess) return err;
+  g_cus[dev].store(cus, std::memory_order_relaxed);
+  return hipSuccess;
+}
+
+// Which kernel, and how it is cut.  The row counts of the experts are on the
+// device, so the choice goes by the average over the experts that can have
+// rows.  Measured on 256 CUs at K = 7168, a round of workgroups (one per CU)
+// takes about 4.8 us times
+//   few-rows kernel   RF + JT   (N 2048: 1 row 11 us with 16 x 16, 26 us with
+//                                64 x 64; 256 rows 30 us with 64 x 32, 58 us with 16 x 64)
+//   tile kernel       6 + JV    (N 2048, 2048 rows: 44 us with 96-row tiles in one
+//                                round, 73 us with 288; 4096 rows: 88 us with 96-row tiles
+//                                in two rounds, 61 us with 128)
+// and the cheapest of them is taken.  Experts of at most 8 rows whose n tiles
+// give every CU several workgroups go to the streaming kernel instead (256
+// experts of 8 rows, N 4096: 1.11 ms, tiles 1.16 ms; of 16 rows: 1.30 against 1.19 ms).
+struct Fp8Plan {
+  int kind;    // 0 stream, 1 few rows, 2 tiles
+  int rf, jt, bm;
+};
+
+Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
+  const int64_t live = a.E < a.M ? a.E : a.M;
+  const double avg = (double)a.M / live;
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  // m tiles of bm rows; an expert's last one is half full on average
+  auto m_tiles = [&](int bm) {
+    if (!a.offsets) return (double)up(a.M, bm);
+    const double per = avg / bm + 0.5;
+    return live * (per > 1.0 ? per : 1.0);
+  };
+  auto rounds = [&](double tiles, int64_t n_tiles) { return (double)(int64_t)((tiles * n_tiles + cus - 1) / cus); };
+  if (avg <= 8.0 && live * up(a.N, kStN) >= 4 * (int64_t)cus) return Fp8Plan{0, 0, 1, 0};
+  Fp8Plan best{2, 0, 0, kTlM};
+  double cost = 1e30;
+  for (int bm = kTlM; bm >= kTlMin; bm -= 32) {
+    const double tiles = m_tiles(bm);
+    const double jv = (double)up((int64_t)(a.M / tiles + 0.999), 32);
+    const double c = rounds(tiles, up(a.N, kTlN)) * (6.0 + (jv > 3.0 ? jv : 3.0));
+    if (c < cost) { cost = c; best = Fp8Plan{2, 0, 0, bm}; }
+  }
+  static const int kShape[6][2] = {{1, 1}, {2, 1}, {4, 1}, {2, 2}, {4, 2}, {4, 4}};
+  for (const auto& s : kShape) {
+    const double c = rounds(m_tiles(16 * s[1]), up(a.N, 16 * s[0])) * (s[0] + s[1]);
+    if (c < cost) { cost = c; best = Fp8Plan{1, s[0], s[1], 0}; }
+  }
+  return best;
+}
+
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
@@ -802,13 +867,22 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   p.K = (int)a.K; p.KB = (int)((a.K + 127) / 128); p.NB = (int)((a.N + 127) / 128);
   p.b_q = a.b_q; p.b_sf = a.b_sf; p.c = static_cast<uint16_t*>(a.c);
   p.n_groups = 0;
-  // few rows an expert: the weights' bytes count.  Where the experts' n tiles
-  // fill the chip their rows are streamed whole, else K is split eight ways.
-  const bool fill = (a.E < a.M ? a.E : a.M) * ((a.N + kStN - 1) / kStN) >= 512;
-  if (a.M <= 8 * (int64_t)a.E) return fill ? launch_stream<1>(a, p, stream) : launch_skinny<1>(a, p, stream);
-  if (a.M <= 24 * (int64_t)a.E) return fill ? launch_stream<2>(a, p, stream) : launch_skinny<2>(a, p, stream);
-  if (a.M <= 64 * (int64_t)a.E) return launch_skinny<4>(a, p, stream);
-  return a.M <= kTlM * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
+  int cus = 0;
+  const hipError_t err = device_cus(cus);
+  if (err != hipSuccess) return err;
+  const Fp8Plan plan = plan_of(a, cus);
+  p.bm = plan.bm;
+  if (plan.kind == 0) return launch_stream<1>(a, p, stream);
+  if (plan.kind == 2)   // weights past the caches where an expert is one tile on average
+    return a.M <= plan.bm * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
+  switch (plan.rf * 8 + plan.jt) {
+    case 9: return launch_skinny<1, 1, 4>(a, p, stream);
+    case 17: return launch_skinny<2, 1, 4>(a, p, stream);
+    case 33: return launch_skinny<4, 1, 3>(a, p, stream);
+    case 18: return launch_skinny<2, 2, 3>(a, p, stream);
+    case 34: return launch_skinny<4, 2, 2>(a, p, stream);
+    default: return launch_skinny<4, 4, 2>(a, p, stream);
+  }
 }
 
 }  // namespace nvfp4

@@ -229,6 +229,46 @@ def test_product_dense(M, N, K):
     _check(c, ref, mag, peak, K, M)
 
 
+# Sizes at which each of the product's kernels is the one taken on 256 CUs: m
+# tiles of 32*jv rows, one a CU; ragged experts of tiles that hold one expert
+# or more; experts of few rows, many of them.
+
+@pytest.mark.parametrize("jv", range(3, 10))
+@pytest.mark.parametrize("N,K", [(200, 272), (72, 16)])
+def test_product_dense_tiles(jv, N, K):
+    M = 256 * 32 * jv - 19
+    print(f"[case] fp8 dense tiles jv={jv} M={M} N={N} K={K}", flush=True)
+    a, asf, b, bsf = _operands(np.random.default_rng(jv), M, 1, N, K, special=True)
+    c = nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf))
+    ref, mag, peak = P.grouped_product(P.decode(a, asf), [P.decode(b[0], bsf[0], 128)], [0, M], np.arange(M))
+    _check(c, ref, mag, peak, K, M)
+
+
+@pytest.mark.parametrize("K", [128, 144, 384, 512, 1040, 1168])
+def test_product_grouped_tiles(K):
+    rng = np.random.default_rng(K)
+    counts = rng.integers(0, 330, 200).tolist()
+    counts[3:6] = [0, 1, 700]
+    _run(counts, 72, K, k=2, extra=5, gather=K % 3 == 2, special=True, bad=True)
+
+
+@pytest.mark.parametrize("N,K", [(200, 16), (250, 144), (129, 640), (256, 1040), (180, 784)])
+def test_product_streamed_experts(N, K):
+    rng = np.random.default_rng(N + K)
+    counts = np.minimum(rng.poisson(4, 600), 40)
+    counts[[0, 7, 599]] = [37, 0, 16]
+    _run(counts.tolist(), N, K, k=3, extra=4, gather=K > 700, special=True, bad=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 2048, 1040), (40, 2048, 400), (100, 1500, 272), (300, 2040, 272), (500, 2000, 144)])
+def test_product_few_rows_shapes(M, N, K):
+    print(f"[case] fp8 few rows M={M} N={N} K={K}", flush=True)
+    a, asf, b, bsf = _operands(np.random.default_rng(M + N), M, 1, N, K)
+    c = nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf))
+    ref, mag, peak = P.grouped_product(P.decode(a, asf), [P.decode(b[0], bsf[0], 128)], [0, M], np.arange(M))
+    _check(c, ref, mag, peak, K, M)
+
+
 def test_product_layer_shape_against_sampled_columns():
     """A layer's own depth and width (K 7168, N 4096) with ragged experts: all
     rows, columns of every 64-wide group."""
