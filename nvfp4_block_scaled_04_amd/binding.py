@@ -512,6 +512,23 @@ def mx_expert_weights(w: ExpertWeights, keep_rowmajor=True):
 FP8 = torch.float8_e4m3fn      # codes of the FP8 entry points (OCP E4M3)
 
 
+# The raw stream of a device without the Stream object around it (a microsecond
+# a call, which small batches feel); torch.cuda.current_stream where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev):
+    return _raw_stream(dev.index) if _raw_stream is not None else _stream(dev)
+
+
+def _is(t, dtype, name, shape):
+    """_dev for a tensor of a known shape, with the usual case first."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t
+    return _dev(t, dtype, name, shape)
+
+
 def _call(name, tensors, *args):
     """Call entry point `name` with `args` and the current stream of the device
     that holds the tensors (all on one device), with that device current."""
@@ -519,12 +536,12 @@ def _call(name, tensors, *args):
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError(f"{name}: all tensors must be on one device")
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(dev))
+        st = fn(*args, _stream_of(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev))
+            st = fn(*args, _stream_of(dev))
     if st != 0:
         raise Nvfp4Error(st, name)
 
@@ -533,7 +550,7 @@ def _out(t, shape, dtype, device, name="out"):
     """The caller's output tensor, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    return _dev(t, dtype, name, shape)
+    return _is(t, dtype, name, shape)
 
 
 def _scale_blocks(n):
@@ -548,8 +565,8 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be 2-D")
     T, k = topk_ids.shape
-    _dev(topk_w, torch.float32, "topk_w", (T, k))
-    _dev(dw, torch.float32, "dw", (T, k))
+    _is(topk_w, torch.float32, "topk_w", (T, k))
+    _is(dw, torch.float32, "dw", (T, k))
     o = _out(out, (T, E), torch.float32, topk_ids.device)
     _call("nvfp4_router_topk_bwd", (topk_ids, topk_w, dw, o), _ptr(topk_ids), _ptr(topk_w), _ptr(dw),
           T, E, k, _ptr(o))
@@ -563,7 +580,7 @@ def moe_dispatch(x, inv_perm, offsets, k, out=None):
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     T, H = x.shape
-    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+    _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _dev(offsets, torch.int32, "offsets")
     o = _out(out, (T * k, H), torch.bfloat16, x.device)
     _call("nvfp4_moe_dispatch", (x, inv_perm, offsets, o), _ptr(x), _ptr(inv_perm), _ptr(offsets), T,
@@ -578,7 +595,7 @@ def moe_dispatch_bwd(drows, inv_perm, offsets, k, out=None):
     if drows.dim() != 2 or k < 1 or drows.shape[0] % k:
         raise ValueError("drows must be 2-D with T*k rows")
     T, H = drows.shape[0] // k, drows.shape[1]
-    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+    _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _dev(offsets, torch.int32, "offsets")
     o = _out(out, (T, H), torch.bfloat16, drows.device)
     _call("nvfp4_moe_dispatch_bwd", (drows, inv_perm, offsets, o), _ptr(drows), _ptr(inv_perm),
@@ -597,10 +614,10 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
         raise ValueError("dout and topk_w must be 2-D")
     T, H = dout.shape
     k = topk_w.shape[1]
-    _dev(topk_w, torch.float32, "topk_w", (T, k))
+    _is(topk_w, torch.float32, "topk_w", (T, k))
     if need_dw:
-        _dev(y, torch.bfloat16, "y", (T * k, H))
-    _dev(inv_perm, torch.int32, "inv_perm", (T * k,))
+        _is(y, torch.bfloat16, "y", (T * k, H))
+    _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _dev(offsets, torch.int32, "offsets")
     dy, dw = out if out is not None else (None, None)
     dy = _out(dy, (T * k, H), torch.bfloat16, dout.device, "dy")
@@ -673,10 +690,10 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
     R, K = a.shape
     E, N, _ = b.shape
     kb = _scale_blocks(K)
-    _dev(a_sf, torch.float32, "a_sf", (R, kb))
-    _dev(b_sf, torch.float32, "b_sf", (E, _scale_blocks(N), kb))
+    _is(a_sf, torch.float32, "a_sf", (R, kb))
+    _is(b_sf, torch.float32, "b_sf", (E, _scale_blocks(N), kb))
     if offsets is not None:
-        _dev(offsets, torch.int32, "offsets", (E + 1,))
+        _is(offsets, torch.int32, "offsets", (E + 1,))
     rows = R
     if a_row_src is not None:
         _dev(a_row_src, torch.int32, "a_row_src")

@@ -76,6 +76,34 @@ __device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, 
   return left > 0;
 }
 
+// m tiles of at most bm rows of expert e0 + lane (0 behind the last expert),
+// its rows [lo, hi), and the tiles of the lanes up to this one
+__device__ __forceinline__ int lane_tiles(const Fp8Params& p, int bm, int e0, int& lo, int& hi, int& incl) {
+  const int lane = threadIdx.x & 63, e = e0 + lane;
+  lo = p.offsets[e < p.E ? e : p.E];
+  hi = p.offsets[e < p.E ? e + 1 : p.E];
+  const int tiles = hi > lo ? (hi - lo + bm - 1) / bm : 0;
+  incl = tiles;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(incl, o);
+    incl += lane >= o ? v : 0;
+  }
+  return tiles;
+}
+
+// m tiles in all
+__device__ __forceinline__ int count_tiles(const Fp8Params& p, int bm) {
+  if (!p.offsets) return (int)((p.M + bm - 1) / bm);
+  int sum = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int lo, hi, incl;
+    lane_tiles(p, bm, e0, lo, hi, incl);
+    sum += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return sum;
+}
+
 // The mt-th tile of at most bm rows in expert order; false if there are fewer.
 // Lane l scans expert e0 + l, 64 experts at a time.
 __device__ __forceinline__ bool row_tile(const Fp8Params& p, int bm, int mt, RowTile& t) {
@@ -84,18 +112,10 @@ __device__ __forceinline__ bool row_tile(const Fp8Params& p, int bm, int mt, Row
     if (mt >= (p.M + bm - 1) / bm) return false;
     return cut_tile(p, bm, 0, (int)p.M, mt, t);
   }
-  const int lane = threadIdx.x & 63;
   int before = 0;
   for (int e0 = 0; e0 < p.E; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = p.offsets[e < p.E ? e : p.E], hi = p.offsets[e < p.E ? e + 1 : p.E];
-    const int tiles = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o);
-      incl += lane >= o ? v : 0;
-    }
+    int lo, hi, incl;
+    const int tiles = lane_tiles(p, bm, e0, lo, hi, incl);
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (mt < before + total) {
       const int src = __ffsll((unsigned long long)__ballot(before + incl > mt)) - 1;
@@ -191,8 +211,8 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
     const int at = none ? 0 : b * 128;
 #pragma unroll
     for (int f = 0; f < RF; ++f)
-      x.w[f] = join(__builtin_amdgcn_raw_buffer_load_b128(rb, wo[f] | lo, at, 2),
-                    __builtin_amdgcn_raw_buffer_load_b128(rb, (wo[f] + 64) | hi, at, 2));
+      x.w[f] = join(__builtin_amdgcn_raw_buffer_load_b128(rb, wo[f] | lo, at, 0),
+                    __builtin_amdgcn_raw_buffer_load_b128(rb, (wo[f] + 64) | hi, at, 0));
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
       x.t[j] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, to[j] | lo, at, 0),
@@ -289,12 +309,13 @@ struct StLoads {
 };
 
 // weights of K block b into dst; zeros behind the last block
+template <int POL>
 __device__ __forceinline__ void st_load_w(const StLoads& st, int b, uint8_t* dst) {
   const uint32_t c0 = b < st.KB - 1 ? 0 : b == st.KB - 1 ? st.w_cut[0] : kNowhere;
   const uint32_t c1 = b < st.KB - 1 ? 0 : b == st.KB - 1 ? st.w_cut[1] : kNowhere;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rb, lds_addr(dst + c * 1024), 16, st.wo[c] | (c & 1 ? c1 : c0), b < st.KB ? b * 128 : 0, 0, 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rb, lds_addr(dst + c * 1024), 16, st.wo[c] | (c & 1 ? c1 : c0), b < st.KB ? b * 128 : 0, 0, POL);
 }
 
 template <int JT>
@@ -313,13 +334,13 @@ __device__ __forceinline__ void st_load_t(const StLoads& st, int b, StTok<JT>& x
 // Stage b: loads of the weights of b + 3 and the tokens of b + 2, products of
 // b.  cur and nxt are __restrict__: the fragment reads get no wait on the
 // direct loads in flight beyond the one written here.
-template <int JT>
+template <int JT, int POL>
 __device__ __forceinline__ void st_stage(float4v (&acc)[2][JT], const StLoads& st, int b, float sb, const StTok<JT>& x,
                                          StTok<JT>& ahead, const uint8_t* __restrict__ cur,
                                          uint8_t* __restrict__ nxt) {
   st_load_t<JT>(st, b + 2, ahead);
   asm volatile("" ::: "memory");       // the count below relies on this order
-  st_load_w(st, b + 3, nxt);
+  st_load_w<POL>(st, b + 3, nxt);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStRing - 1) * (4 + 3 * JT)) : "memory");
   int8v w[2];
 #pragma unroll
@@ -339,7 +360,7 @@ __device__ __forceinline__ void st_stage(float4v (&acc)[2][JT], const StLoads& s
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-template <int JT>
+template <int JT, int POL>
 __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params p) {
   __shared__ __align__(1024) uint8_t smem[kStWaves * kStRing * kStStage];
   const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
@@ -385,24 +406,24 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   uint8_t *s0 = ring, *s1 = ring + kStStage, *s2 = ring + 2 * kStStage, *s3 = ring + 3 * kStStage;
 
   StTok<JT> x0, x1, x2, x3;
-  st_load_w(st, 0, s0);
+  st_load_w<POL>(st, 0, s0);
   asm volatile("" ::: "memory");
   st_load_t<JT>(st, 0, x0);
   asm volatile("" ::: "memory");
-  st_load_w(st, 1, s1);
+  st_load_w<POL>(st, 1, s1);
   asm volatile("" ::: "memory");
   st_load_t<JT>(st, 1, x1);
   asm volatile("" ::: "memory");
-  st_load_w(st, 2, s2);
+  st_load_w<POL>(st, 2, s2);
   asm volatile("" ::: "memory");
   // four stages a pass, those behind the last on zeros
   auto sb = [&](int b) { return uniform_load(bsf, b < p.KB ? b : 0); };
   for (int b = 0; b < p.KB; b += 4) {
     const float f0 = sb(b), f1 = sb(b + 1), f2 = sb(b + 2), f3 = sb(b + 3);
-    st_stage<JT>(acc, st, b, f0, x0, x2, s0, s3);
-    st_stage<JT>(acc, st, b + 1, f1, x1, x3, s1, s0);
-    st_stage<JT>(acc, st, b + 2, f2, x2, x0, s2, s1);
-    st_stage<JT>(acc, st, b + 3, f3, x3, x1, s3, s2);
+    st_stage<JT, POL>(acc, st, b, f0, x0, x2, s0, s3);
+    st_stage<JT, POL>(acc, st, b + 1, f1, x1, x3, s1, s0);
+    st_stage<JT, POL>(acc, st, b + 2, f2, x2, x0, s2, s1);
+    st_stage<JT, POL>(acc, st, b + 3, f3, x3, x1, s3, s2);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 7) == 0;
@@ -678,23 +699,23 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
       o.y = pack_bf16x2(st.acc[f][j][2], st.acc[f][j][3]);
       *reinterpret_cast<uint2*>(ep + r * kTlEpiStride + 2 * (16 * f + 4 * g)) = o;
     }
+    if (vec) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = 8 * h + (lane >> 3), ch = lane & 7;
-      const uint4 v = *reinterpret_cast<const uint4*>(ep + tok * kTlEpiStride + 16 * ch);
-      const int row = (2 * j + wt) * 16 + tok;
-      const int64_t n = nw + 8 * ch;
-      if (row < t.nrows && n < p.N) {
-        uint16_t* dst = p.c + (t.row0 + row) * p.N + n;
-        if (vec) {
-          *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n + i < p.N) dst[i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int tok = 8 * h + (lane >> 3), ch = lane & 7;
+        const uint4 v = *reinterpret_cast<const uint4*>(ep + tok * kTlEpiStride + 16 * ch);
+        const int row = (2 * j + wt) * 16 + tok;
+        const int64_t n = nw + 8 * ch;
+        if (row < t.nrows && n < p.N) *reinterpret_cast<uint4*>(p.c + (t.row0 + row) * p.N + n) = v;
       }
+    } else {
+      // rows at odd places: a token's 64 columns per store
+      const int left = t.nrows - (2 * j + wt) * 16;
+#pragma unroll 4
+      for (int tok = 0; tok < 16; ++tok)
+        if (tok < left && nw + lane < p.N)
+          p.c[(t.row0 + (2 * j + wt) * 16 + tok) * p.N + nw + lane] =
+              *reinterpret_cast<const uint16_t*>(ep + tok * kTlEpiStride + 2 * lane);
     }
   }
 }
@@ -702,10 +723,13 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
 template <int POL>
 __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  // m tiles go round the XCDs (blocks do), so that the n tiles of one m tile
-  // share its tokens in one L2
-  const int xi = blockIdx.x >> 3, xm = xi / p.n_groups;
-  const int mt = xm * 8 + (blockIdx.x & 7), ng = xi - xm * p.n_groups;
+  // Blocks go round the eight XCDs; each XCD takes a contiguous eighth of the
+  // tiles in m tile order, so that the n tiles of an m tile share its tokens,
+  // and an expert's m tiles its weights, in one L2.
+  const int64_t all = (int64_t)count_tiles(p, p.bm) * p.n_groups, chunk = (all + 7) >> 3;
+  const int64_t at = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= chunk || at >= all) return;
+  const int mt = (int)(at / p.n_groups), ng = (int)(at - (int64_t)mt * p.n_groups);
   RowTile t;
   if (!row_tile(p, p.bm, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
@@ -758,12 +782,12 @@ int64_t tile_bound(const Fp8GemmArgs& a, int bm) {
   return b < a.M ? b : a.M;
 }
 
-template <int JT>
+template <int JT, int POL>
 hipError_t launch_stream(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   p.n_groups = (int)((a.N + kStN - 1) / kStN);
   const int64_t grid = tile_bound(a, 16 * JT) * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  fp8_stream_kernel<JT><<<(unsigned)grid, kStWaves * 64, 0, stream>>>(p);
+  fp8_stream_kernel<JT, POL><<<(unsigned)grid, kStWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -781,7 +805,7 @@ constexpr int kMaxDevices = 64;
 template <int POL>
 hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   p.n_groups = (int)((a.N + kTlN - 1) / kTlN);
-  const int64_t grid = (tile_bound(a, p.bm) + 7) / 8 * 8 * p.n_groups;
+  const int64_t grid = (tile_bound(a, p.bm) * p.n_groups + 7) / 8 * 8;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -815,16 +839,19 @@ hipError_t device_cus(int& cus) {
 
 // Which kernel, and how it is cut.  The row counts of the experts are on the
 // device, so the choice goes by the average over the experts that can have
-// rows.  Measured on 256 CUs at K = 7168, a round of workgroups (one per CU)
-// takes about 4.8 us times
-//   few-rows kernel   RF + JT   (N 2048: 1 row 11 us with 16 x 16, 26 us with
-//                                64 x 64; 256 rows 30 us with 64 x 32, 58 us with 16 x 64)
-//   tile kernel       6 + JV    (N 2048, 2048 rows: 44 us with 96-row tiles in one
-//                                round, 73 us with 288; 4096 rows: 88 us with 96-row tiles
-//                                in two rounds, 61 us with 128)
-// and the cheapest of them is taken.  Experts of at most 8 rows whose n tiles
-// give every CU several workgroups go to the streaming kernel instead (256
-// experts of 8 rows, N 4096: 1.11 ms, tiles 1.16 ms; of 16 rows: 1.30 against 1.19 ms).
+// rows.  The cost of each kernel in units of 0.67 ns times K, as measured on 256
+// CUs at K = 7168 (a unit is 4.8 us there):
+//   few rows   (RF + JT) a round of workgroups, one per CU (N 2048: 1 row 11 us
+//              with 16 x 16, 26 us with 64 x 64; 256 rows 30 us with 64 x 32,
+//              58 us with 16 x 64)
+//   tiles      (6 + JV) a round (N 2048: 2048 rows 44 us with 96-row tiles in one
+//              round, 73 us with 288; 4096 rows 88 us with 96-row tiles in
+//              two rounds, 61 us with 128)
+//   streaming  3.2 + B/60 for B workgroups (1 row, N 32768: 36 us; the others
+//              47 us and more)
+// and none is faster than its experts' weights come from HBM: N * live / 4100
+// units (256 experts, N 4096, 8 rows each: streaming 1.11 ms, tiles 1.19 ms; 16
+// rows each: 1.30 ms, 1.19 ms).
 struct Fp8Plan {
   int kind;    // 0 stream, 1 few rows, 2 tiles
   int rf, jt, bm;
@@ -841,18 +868,21 @@ Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
     return live * (per > 1.0 ? per : 1.0);
   };
   auto rounds = [&](double tiles, int64_t n_tiles) { return (double)(int64_t)((tiles * n_tiles + cus - 1) / cus); };
-  if (avg <= 8.0 && live * up(a.N, kStN) >= 4 * (int64_t)cus) return Fp8Plan{0, 0, 1, 0};
-  Fp8Plan best{2, 0, 0, kTlM};
-  double cost = 1e30;
+  const double hbm = (double)live * a.N / 4100.0 * (256.0 / cus);
+  auto over_hbm = [&](double c) { return c > hbm ? c : hbm * 1.02; };
+  const double blocks = m_tiles(16) * up(a.N, kStN) * (256.0 / cus);
+  const double first = 3.2 + blocks / 60, flow = m_tiles(16) * a.N / 4400.0 * (256.0 / cus);
+  double cost = first > flow ? first : flow;
+  Fp8Plan best{0, 0, 1, 0};
   for (int bm = kTlM; bm >= kTlMin; bm -= 32) {
     const double tiles = m_tiles(bm);
     const double jv = (double)up((int64_t)(a.M / tiles + 0.999), 32);
-    const double c = rounds(tiles, up(a.N, kTlN)) * (6.0 + (jv > 3.0 ? jv : 3.0));
+    const double c = over_hbm(rounds(tiles, up(a.N, kTlN)) * (6.0 + (jv > 3.0 ? jv : 3.0)));
     if (c < cost) { cost = c; best = Fp8Plan{2, 0, 0, bm}; }
   }
   static const int kShape[6][2] = {{1, 1}, {2, 1}, {4, 1}, {2, 2}, {4, 2}, {4, 4}};
   for (const auto& s : kShape) {
-    const double c = rounds(m_tiles(16 * s[1]), up(a.N, 16 * s[0])) * (s[0] + s[1]);
+    const double c = over_hbm(rounds(m_tiles(16 * s[1]), up(a.N, 16 * s[0])) * (s[0] + s[1]));
     if (c < cost) { cost = c; best = Fp8Plan{1, s[0], s[1], 0}; }
   }
   return best;
@@ -872,9 +902,13 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   if (err != hipSuccess) return err;
   const Fp8Plan plan = plan_of(a, cus);
   p.bm = plan.bm;
-  if (plan.kind == 0) return launch_stream<1>(a, p, stream);
-  if (plan.kind == 2)   // weights past the caches where an expert is one tile on average
-    return a.M <= plan.bm * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
+  // Weights read once go past the caches, unless rows are no multiple of 128
+  // bytes: two K blocks then share a line, which would be fetched twice (40
+  // experts of 115 rows, N 1001, K 1040: 24 us, 32 us past the caches).
+  const bool aligned = a.K % 128 == 0;
+  if (plan.kind == 0) return aligned ? launch_stream<1, 2>(a, p, stream) : launch_stream<1, 0>(a, p, stream);
+  if (plan.kind == 2)   // once: where an expert is one tile on average
+    return aligned && a.M <= plan.bm * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
   switch (plan.rf * 8 + plan.jt) {
     case 9: return launch_skinny<1, 1, 4>(a, p, stream);
     case 17: return launch_skinny<2, 1, 4>(a, p, stream);
