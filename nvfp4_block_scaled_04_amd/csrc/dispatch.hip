@@ -35,14 +35,33 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
                pack_bf16x2(x[6], x[7])};
 }
 
-// Token of this thread group and the thread's index in it.  A group is TPT
-// threads; short rows put several tokens in one workgroup of kGroupThreads.
+// Token of this thread group (whole waves, so it is made uniform) and the
+// thread's index in it.  A group is TPT threads; short rows put several
+// tokens in one workgroup of kGroupThreads.
 constexpr int kGroupThreads = 256;
 template <int TPT>
 __device__ __forceinline__ int64_t my_token(int& tid) {
   constexpr int per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT;
   tid = threadIdx.x % TPT;
-  return (int64_t)blockIdx.x * per + threadIdx.x / TPT;
+  return (int64_t)blockIdx.x * per + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
+}
+
+// Reads of a token's slots through the constant address space: scalar loads,
+// all in flight together, so that which rows are routed is known in scalar
+// registers before the first row is touched.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) T*)p)[i];
+}
+
+// Rows of slots j0 .. j0 + kBatch - 1: -1 behind slot k - 1 and outside [0, M)
+__device__ __forceinline__ void slot_rows(const int32_t* inv, int64_t t, int k, int j0, int64_t M,
+                                          int32_t (&d)[kBatch]) {
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) d[b] = uniform_load(inv, t * k + (j0 + b < k ? j0 + b : k - 1));
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b)
+    if (j0 + b >= k || d[b] < 0 || d[b] >= M) d[b] = -1;
 }
 
 template <int TPT>
@@ -52,14 +71,16 @@ __global__ __launch_bounds__(TPT >= kGroupThreads ? TPT : kGroupThreads) void di
   int tid;
   const int64_t t = my_token<TPT>(tid);
   if (t >= T) return;
-  const int32_t n = n_valid[0];
+  const int32_t n = uniform_load(n_valid, 0);
   const int64_t M = T * k;
   for (int v = tid; v < hv; v += TPT) {
     const u32x4 a = load_nt(x + t * hv + v);
-    for (int j = 0; j < k; ++j) {
-      const int32_t d = inv[t * k + j];
-      const u32x4 o = d < n ? a : u32x4{0, 0, 0, 0};
-      if (d >= 0 && d < M) store_nt(o, rows + (int64_t)d * hv + v);
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+      int32_t d[kBatch];
+      slot_rows(inv, t, k, j0, M, d);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (d[b] >= 0) store_nt(d[b] < n ? a : u32x4{0, 0, 0, 0}, rows + (int64_t)d[b] * hv + v);
     }
   }
 }
@@ -72,16 +93,17 @@ __global__ __launch_bounds__(TPT >= kGroupThreads ? TPT : kGroupThreads) void di
   const int64_t t = my_token<TPT>(tid);
   if (t >= T) return;
   const int64_t M = T * k;
-  const int32_t n = (int32_t)(n_valid[0] < M ? n_valid[0] : M);
+  const int32_t n = uniform_load(n_valid, 0);
   for (int v = tid; v < hv; v += TPT) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int j0 = 0; j0 < k; j0 += kBatch) {
+      int32_t d[kBatch];
+      slot_rows(inv, t, k, j0, M, d);
       u32x4 r[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int32_t d = j0 + b < k ? inv[t * k + j0 + b] : -1;
         r[b] = u32x4{0, 0, 0, 0};
-        if (d >= 0 && d < n) r[b] = load_nt(drows + (int64_t)d * hv + v);
+        if (d[b] >= 0 && d[b] < n) r[b] = load_nt(drows + (int64_t)d[b] * hv + v);
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
@@ -107,40 +129,41 @@ __global__ __launch_bounds__(TPT >= kGroupThreads ? TPT : kGroupThreads) void co
   const int64_t t = my_token<TPT>(tid);
   const bool live = t < T;                      // the whole group
   const int64_t M = T * k;
-  const int32_t n = n_valid[0];
+  const int32_t n = uniform_load(n_valid, 0);
   for (int j0 = 0; j0 < k; j0 += kBatch) {
     float dot[kBatch] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (live) {
       int32_t d[kBatch];
       float wj[kBatch];
+      slot_rows(inv, t, k, j0, M, d);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        d[b] = j0 + b < k ? inv[t * k + j0 + b] : -1;
-        if (d[b] >= M) d[b] = -1;
-        wj[b] = d[b] >= 0 && d[b] < n ? w[t * k + j0 + b] : 0.0f;
-      }
+      for (int b = 0; b < kBatch; ++b) wj[b] = uniform_load(w, t * k + (j0 + b < k ? j0 + b : k - 1));
       for (int v = tid; v < hv; v += TPT) {
         u32x4 r[kBatch];
+        const u32x4 gv = dout[t * hv + v];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           r[b] = u32x4{0, 0, 0, 0};
           if (dw && d[b] >= 0 && d[b] < n) r[b] = load_nt(y + (int64_t)d[b] * hv + v);
         }
         float g[8];
-        unpack8(dout[t * hv + v], g);
+        unpack8(gv, g);
+        // the stores first: they need no row of y
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           if (d[b] < 0) continue;
-          float f[8], o[8];
-          unpack8(r[b], f);
-          float s = 0.0f;
+          float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s = fmaf(g[i], f[i], s);
-            o[i] = wj[b] * g[i];
-          }
-          dot[b] += s;
+          for (int i = 0; i < 8; ++i) o[i] = wj[b] * g[i];
           store_nt(d[b] < n ? pack8(o) : u32x4{0, 0, 0, 0}, dy + (int64_t)d[b] * hv + v);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          float f[8], s = 0.0f;
+          unpack8(r[b], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = fmaf(g[i], f[i], s);
+          dot[b] += s;
         }
       }
     }

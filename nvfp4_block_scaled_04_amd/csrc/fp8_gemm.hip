@@ -76,57 +76,66 @@ __device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, 
   return left > 0;
 }
 
-// m tiles of at most bm rows of expert e0 + lane (0 behind the last expert),
-// its rows [lo, hi), and the tiles of the lanes up to this one
-__device__ __forceinline__ int lane_tiles(const Fp8Params& p, int bm, int e0, int& lo, int& hi, int& incl) {
-  const int lane = threadIdx.x & 63, e = e0 + lane;
-  lo = p.offsets[e < p.E ? e : p.E];
-  hi = p.offsets[e < p.E ? e + 1 : p.E];
-  const int tiles = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-  incl = tiles;
+// Wave-wide sum of v over the lanes up to this one.
+__device__ __forceinline__ int scan64(int v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o);
-    incl += lane >= o ? v : 0;
+    const int u = __shfl_up(v, o);
+    v += lane >= o ? u : 0;
   }
-  return tiles;
+  return v;
 }
 
-// m tiles in all
-__device__ __forceinline__ int count_tiles(const Fp8Params& p, int bm) {
-  if (!p.offsets) return (int)((p.M + bm - 1) / bm);
-  int sum = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int lo, hi, incl;
-    lane_tiles(p, bm, e0, lo, hi, incl);
-    sum += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return sum;
-}
+// The m tiles of at most bm rows, in expert order: first count() their number,
+// then find() the mt-th.  Lane l counts the tiles of the S = ceil(E / 64)
+// experts from l * S on (independent loads, one scan); find() then scans the
+// S experts of the lane that holds the tile.
+struct TileList {
+  int S, incl, own;
 
-// The mt-th tile of at most bm rows in expert order; false if there are fewer.
-// Lane l scans expert e0 + l, 64 experts at a time.
-__device__ __forceinline__ bool row_tile(const Fp8Params& p, int bm, int mt, RowTile& t) {
-  if (!p.offsets) {
-    t.e = 0;
-    if (mt >= (p.M + bm - 1) / bm) return false;
-    return cut_tile(p, bm, 0, (int)p.M, mt, t);
+  __device__ __forceinline__ static int tiles(int lo, int hi, int bm) {
+    return hi > lo ? (hi - lo + bm - 1) / bm : 0;
   }
-  int before = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int lo, hi, incl;
-    const int tiles = lane_tiles(p, bm, e0, lo, hi, incl);
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    if (mt < before + total) {
-      const int src = __ffsll((unsigned long long)__ballot(before + incl > mt)) - 1;
-      const int i = mt - before - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(tiles, src));
-      const int first = __builtin_amdgcn_readlane(lo, src);
-      t.e = e0 + src;
-      return cut_tile(p, bm, first, __builtin_amdgcn_readlane(hi, src) - first, i, t);
+  __device__ __forceinline__ int count(const Fp8Params& p, int bm) {
+    if (!p.offsets) return (int)((p.M + bm - 1) / bm);
+    S = (p.E + 63) >> 6;
+    own = 0;
+    const int e0 = (threadIdx.x & 63) * S;
+#pragma unroll 4
+    for (int i = 0; i < S; ++i) {
+      const int e = e0 + i < p.E ? e0 + i : p.E, e1 = e < p.E ? e + 1 : p.E;
+      own += tiles(p.offsets[e], p.offsets[e1], bm);
     }
-    before += total;
+    incl = scan64(own);
+    return __builtin_amdgcn_readlane(incl, 63);
   }
-  return false;
+  __device__ __forceinline__ bool find(const Fp8Params& p, int bm, int mt, RowTile& t) const {
+    if (!p.offsets) {
+      t.e = 0;
+      if (mt >= (p.M + bm - 1) / bm) return false;
+      return cut_tile(p, bm, 0, (int)p.M, mt, t);
+    }
+    if (mt >= __builtin_amdgcn_readlane(incl, 63)) return false;
+    const int at = __ffsll((unsigned long long)__ballot(incl > mt)) - 1;
+    int rest = mt - (__builtin_amdgcn_readlane(incl, at) - __builtin_amdgcn_readlane(own, at));
+    const int lane = threadIdx.x & 63;
+    int e = at * S + lane;
+    if (lane >= S || e >= p.E) e = p.E;
+    const int lo = p.offsets[e], hi = p.offsets[e < p.E ? e + 1 : p.E], n = tiles(lo, hi, bm);
+    const int sum = scan64(n);
+    const int src = __ffsll((unsigned long long)__ballot(sum > rest)) - 1;
+    rest -= __builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(n, src);
+    const int first = __builtin_amdgcn_readlane(lo, src);
+    t.e = at * S + src;
+    return cut_tile(p, bm, first, __builtin_amdgcn_readlane(hi, src) - first, rest, t);
+  }
+};
+
+__device__ __forceinline__ bool row_tile(const Fp8Params& p, int bm, int mt, RowTile& t) {
+  TileList list;
+  list.count(p, bm);
+  return list.find(p, bm, mt, t);
 }
 
 // A row of tile row i, or -1 (behind the tile, or an index outside A)
@@ -726,12 +735,13 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   // Blocks go round the eight XCDs; each XCD takes a contiguous eighth of the
   // tiles in m tile order, so that the n tiles of an m tile share its tokens,
   // and an expert's m tiles its weights, in one L2.
-  const int64_t all = (int64_t)count_tiles(p, p.bm) * p.n_groups, chunk = (all + 7) >> 3;
+  TileList list;
+  const int64_t all = (int64_t)list.count(p, p.bm) * p.n_groups, chunk = (all + 7) >> 3;
   const int64_t at = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
   if ((blockIdx.x >> 3) >= chunk || at >= all) return;
   const int mt = (int)(at / p.n_groups), ng = (int)(at - (int64_t)mt * p.n_groups);
   RowTile t;
-  if (!row_tile(p, p.bm, mt, t)) return;
+  if (!list.find(p, p.bm, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
   t.nrows = __builtin_amdgcn_readfirstlane(t.nrows);
   t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
