@@ -512,19 +512,17 @@ def mx_expert_weights(w: ExpertWeights, keep_rowmajor=True):
 FP8 = torch.float8_e4m3fn      # codes of the FP8 entry points (OCP E4M3)
 
 
-# The raw stream of a device without the Stream object around it (a microsecond
-# a call, which small batches feel); torch.cuda.current_stream where it is missing.
+# The current device and its raw stream without the Python objects around them
+# (two microseconds a call, which small batches feel), or with them where torch
+# does not offer these.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream_of(dev):
-    return _raw_stream(dev.index) if _raw_stream is not None else _stream(dev)
-
-
-def _is(t, dtype, name, shape):
-    """_dev for a tensor of a known shape, with the usual case first."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
-            and t.is_contiguous()):
+def _is(t, dtype, name, shape=None):
+    """_dev, with the usual case first."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
         return t
     return _dev(t, dtype, name, shape)
 
@@ -532,16 +530,16 @@ def _is(t, dtype, name, shape):
 def _call(name, tensors, *args):
     """Call entry point `name` with `args` and the current stream of the device
     that holds the tensors (all on one device), with that device current."""
-    dev = tensors[0].device
+    at = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name}: all tensors must be on one device")
     fn = getattr(_lib or lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream_of(dev))
+    if at == _raw_device():
+        st = fn(*args, _raw_stream(at) if _raw_stream is not None else _stream(at))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream_of(dev))
+        with torch.cuda.device(at):
+            st = fn(*args, _stream(at))
     if st != 0:
         raise Nvfp4Error(st, name)
 
@@ -561,7 +559,7 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
     """Gradient of router_topk's weights with respect to the logits: topk_ids
     (T, k) int32, topk_w (T, k) float32 as router_topk returned them, dw (T, k)
     float32 -> dlogits (T, E) float32 (zero for experts not chosen)."""
-    _dev(topk_ids, torch.int32, "topk_ids")
+    _is(topk_ids, torch.int32, "topk_ids")
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be 2-D")
     T, k = topk_ids.shape
@@ -576,12 +574,12 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
 def moe_dispatch(x, inv_perm, offsets, k, out=None):
     """x (T, H) bf16 -> rows (T*k, H) bf16 in expert order: row inv_perm[t*k+j]
     is token t; rows from offsets[E] on (invalid expert ids) are zero."""
-    _dev(x, torch.bfloat16, "x")
+    _is(x, torch.bfloat16, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     T, H = x.shape
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
-    _dev(offsets, torch.int32, "offsets")
+    _is(offsets, torch.int32, "offsets")
     o = _out(out, (T * k, H), torch.bfloat16, x.device)
     _call("nvfp4_moe_dispatch", (x, inv_perm, offsets, o), _ptr(x), _ptr(inv_perm), _ptr(offsets), T,
           k, offsets.numel() - 1, H, _ptr(o))
@@ -591,12 +589,12 @@ def moe_dispatch(x, inv_perm, offsets, k, out=None):
 def moe_dispatch_bwd(drows, inv_perm, offsets, k, out=None):
     """Gradient of moe_dispatch: drows (T*k, H) bf16 -> dx (T, H) bf16, each
     token's routed row gradients summed in fp32."""
-    _dev(drows, torch.bfloat16, "drows")
+    _is(drows, torch.bfloat16, "drows")
     if drows.dim() != 2 or k < 1 or drows.shape[0] % k:
         raise ValueError("drows must be 2-D with T*k rows")
     T, H = drows.shape[0] // k, drows.shape[1]
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
-    _dev(offsets, torch.int32, "offsets")
+    _is(offsets, torch.int32, "offsets")
     o = _out(out, (T, H), torch.bfloat16, drows.device)
     _call("nvfp4_moe_dispatch_bwd", (drows, inv_perm, offsets, o), _ptr(drows), _ptr(inv_perm),
           _ptr(offsets), T, k, offsets.numel() - 1, H, _ptr(o))
@@ -608,8 +606,8 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
     bf16, dw (T, k) float32).  dy rows from offsets[E] on are zero, and so is dw
     of pairs with an invalid expert id.  need_dw=False: dw is None and y (which
     may be None) is not read.  out: (dy, dw) tensors to write."""
-    _dev(dout, torch.bfloat16, "dout")
-    _dev(topk_w, torch.float32, "topk_w")
+    _is(dout, torch.bfloat16, "dout")
+    _is(topk_w, torch.float32, "topk_w")
     if dout.dim() != 2 or topk_w.dim() != 2:
         raise ValueError("dout and topk_w must be 2-D")
     T, H = dout.shape
@@ -618,7 +616,7 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
     if need_dw:
         _is(y, torch.bfloat16, "y", (T * k, H))
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
-    _dev(offsets, torch.int32, "offsets")
+    _is(offsets, torch.int32, "offsets")
     dy, dw = out if out is not None else (None, None)
     dy = _out(dy, (T * k, H), torch.bfloat16, dout.device, "dy")
     dw = _out(dw, (T, k), torch.float32, dout.device, "dw") if need_dw else None
@@ -636,7 +634,7 @@ def _fp8_rows(name, x, C, offsets, out):
     sf = _out(sf, (R, _scale_blocks(C)), torch.float32, dev, "sf")
     n_rows = None
     if offsets is not None:
-        _dev(offsets, torch.int32, "offsets")
+        _is(offsets, torch.int32, "offsets")
         n_rows = offsets.data_ptr() + 4 * (offsets.numel() - 1)
     ld = x.stride(0) if R > 1 else (x.shape[1] + 7) // 8 * 8   # a one-row tensor's row stride is arbitrary
     _call(name, (x, q, sf, offsets), _ptr(x), R, C, ld, n_rows, _ptr(q), _ptr(sf))
@@ -663,7 +661,7 @@ def fp8_swiglu_quantize(x, offsets=None, out=None):
 def fp8_quantize_weight(w, out=None):
     """w (G, N, K) bf16 -> FP8 codes q (G, N, K) float8_e4m3fn and one float32
     scale per 128 x 128 block, sf (G, ceil(N/128), ceil(K/128))."""
-    _dev(w, torch.bfloat16, "w")
+    _is(w, torch.bfloat16, "w")
     if w.dim() != 3:
         raise ValueError("w must be (groups, N, K)")
     G, N, K = w.shape
@@ -683,8 +681,8 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
     row d; rows from offsets[E] on are not written.  offsets None: a dense
     product with one expert.  M: rows of c (default: the length of a_row_src, or
     R)."""
-    _dev(a, FP8, "a")
-    _dev(b, FP8, "b")
+    _is(a, FP8, "a")
+    _is(b, FP8, "b")
     if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[2]:
         raise ValueError("a must be (R, K) and b (E, N, K)")
     R, K = a.shape
@@ -696,7 +694,7 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
         _is(offsets, torch.int32, "offsets", (E + 1,))
     rows = R
     if a_row_src is not None:
-        _dev(a_row_src, torch.int32, "a_row_src")
+        _is(a_row_src, torch.int32, "a_row_src")
         rows = a_row_src.numel()
     if M is None:
         M = rows

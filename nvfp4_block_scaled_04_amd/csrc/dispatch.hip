@@ -74,7 +74,7 @@ __global__ __launch_bounds__(TPT >= kGroupThreads ? TPT : kGroupThreads) void di
   const int32_t n = uniform_load(n_valid, 0);
   const int64_t M = T * k;
   for (int v = tid; v < hv; v += TPT) {
-    const u32x4 a = load_nt(x + t * hv + v);
+    const u32x4 a = x[t * hv + v];
     for (int j0 = 0; j0 < k; j0 += kBatch) {
       int32_t d[kBatch];
       slot_rows(inv, t, k, j0, M, d);

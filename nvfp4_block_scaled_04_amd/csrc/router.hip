@@ -81,8 +81,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const float* __restric
 // Gradient of the weights with respect to the logits: with w the softmax over
 // the k chosen logits, dlogits[t][ids[t][j]] += w_j (dw_j - sum_i w_i dw_i),
 // 0 for every other expert.  One wave per token: lane j forms term j, lane l
-// then builds dlogits for the four experts 256 i + 4 l .. + 3 in registers,
-// taking the terms in slot order (ids repeated in a row add up in that order;
+// then builds dlogits for four experts of each 256 in registers (4 l .. + 3
+// with 16-byte stores, else l, l + 64, ...), taking the terms in slot order (ids repeated in a row add up in that order;
 // ids outside [0, E) match no expert).  Bound by the 4 E bytes written per
 // token.  VEC: E % 4 == 0, 16-byte stores.
 template <bool VEC>
@@ -109,20 +109,21 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __r
   // every lane takes every pass: the terms are read from lanes that may hold
   // no expert of this pass
   for (int base = 0; base < E; base += 256) {
-    const int e0 = base + 4 * lane;
+    constexpr int kStep = VEC ? 1 : 64;        // between a lane's experts
+    const int e0 = base + (VEC ? 4 * lane : lane);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int j = 0; j < k; ++j) {
       const int e = __builtin_amdgcn_readlane(id, j);
       const float d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(term), j));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += e == e0 + i ? d : 0.0f;
+      for (int i = 0; i < 4; ++i) v[i] += e == e0 + kStep * i ? d : 0.0f;
     }
     if constexpr (VEC) {
       if (e0 < E) *reinterpret_cast<float4*>(dlogits + t * E + e0) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (e0 + i < E) dlogits[t * E + e0 + i] = v[i];
+        if (e0 + kStep * i < E) dlogits[t * E + e0 + kStep * i] = v[i];
     }
   }
 }
