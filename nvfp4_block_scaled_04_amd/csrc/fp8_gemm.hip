@@ -578,32 +578,34 @@ __device__ __forceinline__ void tl_products(TlState<JV>& st, const int8v& tn, fl
 // pointers are __restrict__, and apart within one function: a fragment read
 // is then known not to alias the loads in flight, and gets no wait on them.
 template <int JV, int J>
-__device__ __forceinline__ void tl_first(TlState<JV>& st, const TlLoads& L, int b, float sb,
+__device__ __forceinline__ void tl_first(TlState<JV>& st, const TlLoads& L, int b, float sb, bool on,
                                          const uint8_t* __restrict__ t1, const uint8_t* __restrict__ sf,
                                          uint8_t* __restrict__ nt) {
   using S = TlState<JV>;
   if constexpr (J < S::JH - 1) {
     const int8v tn = tl_frag(t1, st.tok_at0, st.tok_at1, (J + 1) * 4096);
-    const float sn = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    const float v = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    const float sn = on ? v : 0.0f;
     constexpr int steps = S::JH - 1, n2 = S::NT - S::N1;
 #pragma unroll
     for (int c = 0; c < n2; ++c)
       if (c * steps / n2 == J) tl_load_t(L, b + 1, S::N1 + c, nt);
     tl_products<JV, J>(st, tn, sn, nullptr);
-    tl_first<JV, J + 1>(st, L, b, sb, t1, sf, nt);
+    tl_first<JV, J + 1>(st, L, b, sb, on, t1, sf, nt);
   }
 }
 
 // Steps JH-1 .. JV-2: fragments from T2 (t2), loads of the weights and T1 of
 // block b + 2 into this stage's buffers.
 template <int JV, int J, int POL>
-__device__ __forceinline__ void tl_second(TlState<JV>& st, const TlLoads& L, int b, float sb,
+__device__ __forceinline__ void tl_second(TlState<JV>& st, const TlLoads& L, int b, float sb, bool on,
                                           const uint8_t* __restrict__ t2, const uint8_t* __restrict__ sf,
                                           uint8_t* __restrict__ w, uint8_t* __restrict__ t1) {
   using S = TlState<JV>;
   if constexpr (J < JV - 1) {
     const int8v tn = tl_frag(t2, st.tok_at0, st.tok_at1, (J + 1) * 4096);
-    const float sn = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    const float v = *reinterpret_cast<const float*>(sf + st.sf_at + (J + 1) * 512) * sb;
+    const float sn = on ? v : 0.0f;
     constexpr int steps = JV - S::JH, n = 4 + S::N1, at = J - (S::JH - 1);
 #pragma unroll
     for (int c = 0; c < n; ++c)
@@ -612,16 +614,17 @@ __device__ __forceinline__ void tl_second(TlState<JV>& st, const TlLoads& L, int
         else tl_load_t(L, b + 2, c - 4, t1);
       }
     tl_products<JV, J>(st, tn, sn, nullptr);
-    tl_second<JV, J + 1, POL>(st, L, b, sb, t2, sf, w, t1);
+    tl_second<JV, J + 1, POL>(st, L, b, sb, on, t2, sf, w, t1);
   }
 }
 
 // Step JV-1: the next stage's first fragments.
 template <int JV>
-__device__ __forceinline__ void tl_last(TlState<JV>& st, float sb_next, const uint8_t* __restrict__ wn,
+__device__ __forceinline__ void tl_last(TlState<JV>& st, float sb_next, bool on, const uint8_t* __restrict__ wn,
                                         const uint8_t* __restrict__ t1n, const uint8_t* __restrict__ sfn) {
   const int8v tn = tl_frag(t1n, st.tok_at0, st.tok_at1, 0);
-  const float sn = *reinterpret_cast<const float*>(sfn + st.sf_at) * sb_next;
+  const float v = *reinterpret_cast<const float*>(sfn + st.sf_at) * sb_next;
+  const float sn = on ? v : 0.0f;
   tl_products<JV, JV - 1>(st, tn, sn, wn);
 }
 
@@ -650,8 +653,7 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
   const float* bsf = p.b_sf + ((int64_t)t.e * p.NB + nb) * p.KB;
   uint8_t *w0 = smem, *w1 = smem + kTlWBytes, *t0 = smem + 2 * kTlWBytes, *t1 = t0 + kTlTBytes, *sf = t1 + kTlTBytes;
   auto sf_of = [&](int b) { return sf + ((b >> 2) & 1) * kTlSfBytes + (b & 3) * 4; };
-  // scale of block b's weights; 0 for the block of zeros behind an odd count
-  auto sb_of = [&](int b) { const float v = uniform_load(bsf, b < KB ? b : 0); return b < KB ? v : 0.0f; };
+  auto sb_of = [&](int b) { return uniform_load(bsf, b < KB ? b : 0); };
 
 #pragma unroll
   for (int c = 0; c < 4; ++c) tl_load_w<POL>(L, 0, c, w0);
@@ -673,17 +675,19 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
   st.s = *reinterpret_cast<const float*>(sf + st.sf_at) * sb_of(0);
 
   auto stage = [&](int b, uint8_t* wc, uint8_t* tc, uint8_t* wx, uint8_t* tx) {
+    // behind an odd number of blocks one of zeros is run: what its scales'
+    // place holds (another row's, maybe no number) must not count
     const float sb = sb_of(b), sb_next = sb_of(b + 1);
+    const bool on = b < KB, on_next = b + 1 < KB;
     if ((b & 3) == 0) tl_load_s(L, b + 4, sf + (((b >> 2) + 1) & 1) * kTlSfBytes);
-    tl_first<JV, 0>(st, L, b, sb, tc, sf_of(b), tx);
+    tl_first<JV, 0>(st, L, b, sb, on, tc, sf_of(b), tx);
     NVFP4_TL_WAIT(S::kLoads);
     bare_barrier();
-    tl_second<JV, S::JH - 1, POL>(st, L, b, sb, tc, sf_of(b), wc, tc);
+    tl_second<JV, S::JH - 1, POL>(st, L, b, sb, on, tc, sf_of(b), wc, tc);
     NVFP4_TL_WAIT(S::kLoads);
     bare_barrier();
-    tl_last<JV>(st, sb_next, wx, tx, sf_of(b + 1));
+    tl_last<JV>(st, sb_next, on_next, wx, tx, sf_of(b + 1));
   };
-  // an odd number of blocks runs one more of zeros
   for (int b = 0; b < KB; b += 2) {
     stage(b, w0, t0, w1, t1);
     stage(b + 1, w1, t1, w0, t0);

@@ -369,3 +369,30 @@ def test_product_and_quantise_replay_from_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)), r
         assert np.array_equal(_codes(hq[0]), want[1]) and np.array_equal(host(hq[1]), want[2])
+
+
+@pytest.mark.parametrize("K", [272, 640, 784, 1040])
+@pytest.mark.parametrize("counts", [[30, 2], [3] * 700, [250] * 200])
+def test_product_bad_row_stays_its_own(counts, K):
+    """NaN and infinite scales of one A row, and of rows that no expert takes,
+    reach no other row (odd numbers of K blocks, a gather of neighbours)."""
+    print(f"[case] fp8 bad rows K={K} experts={len(counts)}", flush=True)
+    rng = np.random.default_rng(K)
+    M, E, N = sum(counts), len(counts), 72
+    R = M + 3
+    a, asf, b, bsf = _operands(rng, R, E, N, K)
+    asf[5], asf[M - 2], asf[M:] = np.nan, np.inf, np.nan
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    src = rng.permutation(M).astype(np.int32)
+    ops = _dev(a, asf, b, bsf)
+    for s in (src, None):
+        c = nv.fp8_grouped_gemm(*ops, offsets=torch.from_numpy(off).to(DEV), M=M,
+                                a_row_src=None if s is None else torch.from_numpy(s).to(DEV))
+        rows = np.arange(M) if s is None else s
+        good = np.isfinite(asf[rows]).all(1)
+        clean = np.where(np.isfinite(asf), asf, 0).astype(np.float32)
+        ref, mag, peak = P.grouped_product(P.decode(a, clean), [P.decode(b[e], bsf[e], 128) for e in range(E)], off, rows)
+        got = bf16_values(host(c))
+        assert np.isfinite(got[good]).all() and not np.isfinite(got[~good]).any()
+        sums = (128 + 2 + K // 128 + 9) * 2.0 ** -23 * mag + 7 * 2.0 ** -13 * peak
+        assert np.all((np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * sums)[good])
