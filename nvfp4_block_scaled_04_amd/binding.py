@@ -544,10 +544,10 @@ def _call(name, tensors, *args):
         raise Nvfp4Error(st, name)
 
 
-def _out(t, shape, dtype, device, name="out"):
-    """The caller's output tensor, checked, or a new one."""
+def _out(t, shape, dtype, like, name="out"):
+    """The caller's output tensor, checked, or a new one on like's device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     return _is(t, dtype, name, shape)
 
 
@@ -565,7 +565,7 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
     T, k = topk_ids.shape
     _is(topk_w, torch.float32, "topk_w", (T, k))
     _is(dw, torch.float32, "dw", (T, k))
-    o = _out(out, (T, E), torch.float32, topk_ids.device)
+    o = _out(out, (T, E), torch.float32, topk_ids)
     _call("nvfp4_router_topk_bwd", (topk_ids, topk_w, dw, o), _ptr(topk_ids), _ptr(topk_w), _ptr(dw),
           T, E, k, _ptr(o))
     return o
@@ -580,7 +580,7 @@ def moe_dispatch(x, inv_perm, offsets, k, out=None):
     T, H = x.shape
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _is(offsets, torch.int32, "offsets")
-    o = _out(out, (T * k, H), torch.bfloat16, x.device)
+    o = _out(out, (T * k, H), torch.bfloat16, x)
     _call("nvfp4_moe_dispatch", (x, inv_perm, offsets, o), _ptr(x), _ptr(inv_perm), _ptr(offsets), T,
           k, offsets.numel() - 1, H, _ptr(o))
     return o
@@ -595,7 +595,7 @@ def moe_dispatch_bwd(drows, inv_perm, offsets, k, out=None):
     T, H = drows.shape[0] // k, drows.shape[1]
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _is(offsets, torch.int32, "offsets")
-    o = _out(out, (T, H), torch.bfloat16, drows.device)
+    o = _out(out, (T, H), torch.bfloat16, drows)
     _call("nvfp4_moe_dispatch_bwd", (drows, inv_perm, offsets, o), _ptr(drows), _ptr(inv_perm),
           _ptr(offsets), T, k, offsets.numel() - 1, H, _ptr(o))
     return o
@@ -618,8 +618,8 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
     _is(offsets, torch.int32, "offsets")
     dy, dw = out if out is not None else (None, None)
-    dy = _out(dy, (T * k, H), torch.bfloat16, dout.device, "dy")
-    dw = _out(dw, (T, k), torch.float32, dout.device, "dw") if need_dw else None
+    dy = _out(dy, (T * k, H), torch.bfloat16, dout, "dy")
+    dw = _out(dw, (T, k), torch.float32, dout, "dw") if need_dw else None
     _call("nvfp4_moe_combine_bwd", (dout, y if need_dw else None, inv_perm, topk_w, offsets, dy, dw),
           _ptr(dout), _ptr(y) if need_dw else None, _ptr(inv_perm), _ptr(topk_w), _ptr(offsets), T, k,
           offsets.numel() - 1, H, _ptr(dy), _ptr(dw))
@@ -628,10 +628,9 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
 
 def _fp8_rows(name, x, C, offsets, out):
     R = x.shape[0]
-    dev = x.device
     q, sf = out if out is not None else (None, None)
-    q = _out(q, (R, C), FP8, dev, "q")
-    sf = _out(sf, (R, _scale_blocks(C)), torch.float32, dev, "sf")
+    q = _out(q, (R, C), FP8, x, "q")
+    sf = _out(sf, (R, _scale_blocks(C)), torch.float32, x, "sf")
     n_rows = None
     if offsets is not None:
         _is(offsets, torch.int32, "offsets")
@@ -666,8 +665,8 @@ def fp8_quantize_weight(w, out=None):
         raise ValueError("w must be (groups, N, K)")
     G, N, K = w.shape
     q, sf = out if out is not None else (None, None)
-    q = _out(q, (G, N, K), FP8, w.device, "q")
-    sf = _out(sf, (G, _scale_blocks(N), _scale_blocks(K)), torch.float32, w.device, "sf")
+    q = _out(q, (G, N, K), FP8, w, "q")
+    sf = _out(sf, (G, _scale_blocks(N), _scale_blocks(K)), torch.float32, w, "sf")
     _call("nvfp4_fp8_quantize_weight", (w, q, sf), _ptr(w), G, N, K, _ptr(q), _ptr(sf))
     return q, sf
 
@@ -700,7 +699,7 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
         M = rows
     elif M > rows:
         raise ValueError(f"M = {M} is more than the {rows} rows of the operand")
-    c = _out(out, (M, N), torch.bfloat16, a.device)
+    c = _out(out, (M, N), torch.bfloat16, a)
     _call("nvfp4_fp8_grouped_gemm", (a, a_sf, b, b_sf, offsets, a_row_src, c), _ptr(a), _ptr(a_sf), R,
           _ptr(a_row_src), a_row_div, _ptr(offsets), E, M, N, K, _ptr(b), _ptr(b_sf), _ptr(c))
     return c

@@ -215,20 +215,19 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
     for (int j = 0; j < JT; ++j) acc[f][j] = float4v{0, 0, 0, 0};
 
   auto load = [&](int b, SkFrag<RF, JT>& x) {
-    const bool none = b >= p.KB, last = b == p.KB - 1;
-    const uint32_t lo = none ? kNowhere : last ? cut_lo : 0, hi = none ? kNowhere : last ? cut_hi : 0;
-    const int at = none ? 0 : b * 128;
+    const bool last = b == p.KB - 1;
+    const uint32_t lo = last ? cut_lo : 0, hi = last ? cut_hi : 0;
 #pragma unroll
     for (int f = 0; f < RF; ++f)
-      x.w[f] = join(__builtin_amdgcn_raw_buffer_load_b128(rb, wo[f] | lo, at, 0),
-                    __builtin_amdgcn_raw_buffer_load_b128(rb, (wo[f] + 64) | hi, at, 0));
+      x.w[f] = join(__builtin_amdgcn_raw_buffer_load_b128(rb, wo[f] | lo, b * 128, 0),
+                    __builtin_amdgcn_raw_buffer_load_b128(rb, (wo[f] + 64) | hi, b * 128, 0));
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
-      x.t[j] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, to[j] | lo, at, 0),
-                    __builtin_amdgcn_raw_buffer_load_b128(ra, (to[j] + 64) | hi, at, 0));
-      x.s[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so[j] | (none ? kNowhere : 0), none ? 0 : b * 4, 0));
+      x.t[j] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, to[j] | lo, b * 128, 0),
+                    __builtin_amdgcn_raw_buffer_load_b128(ra, (to[j] + 64) | hi, b * 128, 0));
+      x.s[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so[j], b * 4, 0));
     }
-    x.sb = uniform_load(bsf, none ? 0 : b);
+    x.sb = uniform_load(bsf, b);
     asm volatile("" ::: "memory");      // issued here, not where they are used
   };
   auto add = [&](const SkFrag<RF, JT>& x) {
@@ -245,12 +244,13 @@ __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) 
   };
   SkFrag<RF, JT> x[D];
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(wave + kSkWaves * d, x[d]);
+  for (int d = 0; d < D; ++d)
+    if (wave + kSkWaves * d < p.KB) load(wave + kSkWaves * d, x[d]);
   for (int b = wave; b < p.KB; b += D * kSkWaves) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      add(x[d]);
-      load(b + kSkWaves * (d + D), x[d]);
+      if (b + kSkWaves * d < p.KB) add(x[d]);
+      if (b + kSkWaves * (d + D) < p.KB) load(b + kSkWaves * (d + D), x[d]);
     }
   }
 
@@ -924,12 +924,12 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   if (plan.kind == 2)   // once: where an expert is one tile on average
     return aligned && a.M <= plan.bm * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
   switch (plan.rf * 8 + plan.jt) {
-    case 9: return launch_skinny<1, 1, 4>(a, p, stream);
-    case 17: return launch_skinny<2, 1, 4>(a, p, stream);
-    case 33: return launch_skinny<4, 1, 3>(a, p, stream);
-    case 18: return launch_skinny<2, 2, 3>(a, p, stream);
+    case 9: return launch_skinny<1, 1, 3>(a, p, stream);
+    case 17: return launch_skinny<2, 1, 3>(a, p, stream);
+    case 33: return launch_skinny<4, 1, 2>(a, p, stream);
+    case 18: return launch_skinny<2, 2, 2>(a, p, stream);
     case 34: return launch_skinny<4, 2, 2>(a, p, stream);
-    default: return launch_skinny<4, 4, 2>(a, p, stream);
+    default: return launch_skinny<4, 4, 1>(a, p, stream);
   }
 }
 
