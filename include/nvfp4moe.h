@@ -484,7 +484,8 @@ nvfp4_status nvfp4_moe_combine_bwd(const void* dout_bf16, const void* y_bf16,
  * nvfp4_fp8_quantize_weight: groups matrices [N][K], contiguous.
  * Shapes: rows, groups, N >= 0; 16 <= cols, K < 2^24, multiples of 16; ld_x
  *   at least the row's width and a multiple of 8; fewer than 2^31 scales in
- *   all.  x, w 16-byte aligned, q 8-byte.  No workspace.
+ *   all.  x, w 16-byte aligned, q 8-byte.  Outputs must not overlap the input
+ *   or each other.  No workspace.
  * ---------------------------------------------------------------------- */
 nvfp4_status nvfp4_fp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld_x,
                                 const int32_t* n_rows, uint8_t* q, float* sf, void* stream);
@@ -502,8 +503,9 @@ nvfp4_status nvfp4_fp8_quantize_weight(const void* w_bf16, int64_t groups, int64
  *                         * sum_{k in block b} a_q[s][k] * b_q[e][n][k] ),
  * fp32 accumulation, blocks of 128 along K (the last may be shorter).
  * expert_offsets == NULL (E must be 1): a dense product, rows 0 .. M-1.
- * Rows d >= off[E] are not written.  Requires off[E] <= M.  An A row index
- * outside [0, rows_a) reads as a row of zeros.
+ * Rows d >= off[E] are not written.  Requires off[E] <= M.  A negative
+ * a_row_src[d], and a row s >= rows_a, reads as a row of zeros.  c must not
+ * overlap the inputs.
  * a_q uint8 [rows_a][K], a_sf float [rows_a][ceil(K/128)] (nvfp4_fp8_quantize);
  * b_q uint8 [E][N][K], b_sf float [E][ceil(N/128)][ceil(K/128)]
  * (nvfp4_fp8_quantize_weight; row-major, no packing); c BF16 [M][N].

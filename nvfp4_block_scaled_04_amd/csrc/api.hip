@@ -669,9 +669,13 @@ nvfp4_status fp8_rows_impl(bool swiglu, const char* what, const void* x, int64_t
   if (rows >= (int64_t(1) << 31) || rows * ((cols + 127) / 128) >= (int64_t(1) << 31))
     return fail(NVFP4_ERR_SHAPE, "tensor too large (2^31 scales or more)");
   if (rows == 0) return NVFP4_OK;
+  if (ld_x >= (int64_t(1) << 60) / rows) return fail(NVFP4_ERR_SHAPE, "rows * ld_x must be below 2^60");
   if (!x || !q || !sf) return fail(NVFP4_ERR_INVALID_ARG, "x, q and sf must be non-NULL");
   if (!aligned(x, 16) || !aligned(q, 8) || !aligned(sf, 4) || (n_rows && !aligned(n_rows, 4)))
     return fail(NVFP4_ERR_INVALID_ARG, "x must be 16-byte, q 8-byte, sf and n_rows 4-byte aligned");
+  const int64_t xb = 2 * ((rows - 1) * ld_x + width), qb = rows * cols, sb = 4 * rows * ((cols + 127) / 128);
+  if (overlap(q, qb, x, xb) || overlap(sf, sb, x, xb) || overlap(q, qb, sf, sb))
+    return fail(NVFP4_ERR_INVALID_ARG, "q and sf must not overlap x or each other");
   nvfp4_status st = check_arch();
   if (st != NVFP4_OK) return st;
   return finish(nvfp4::launch_fp8_rows(swiglu, x, rows, cols, ld_x, n_rows, q, sf,
@@ -779,6 +783,9 @@ nvfp4_status nvfp4_fp8_quantize_weight(const void* w, int64_t groups, int64_t N,
   if (!w || !q || !sf) return fail(NVFP4_ERR_INVALID_ARG, "w, q and sf must be non-NULL");
   if (!aligned(w, 16) || !aligned(q, 8) || !aligned(sf, 4))
     return fail(NVFP4_ERR_INVALID_ARG, "w must be 16-byte, q 8-byte and sf 4-byte aligned");
+  const int64_t n = groups * N * K;
+  if (overlap(q, n, w, 2 * n) || overlap(sf, 4 * groups * per, w, 2 * n) || overlap(q, n, sf, 4 * groups * per))
+    return fail(NVFP4_ERR_INVALID_ARG, "q and sf must not overlap w or each other");
   nvfp4_status st = check_arch();
   if (st != NVFP4_OK) return st;
   return finish(nvfp4::launch_fp8_weight(w, groups, N, K, q, sf, static_cast<hipStream_t>(stream)),
@@ -814,6 +821,12 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64
     return fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte, scales 4-byte and c 2-byte aligned");
   if ((a_row_src && !aligned(a_row_src, 4)) || (expert_offsets && !aligned(expert_offsets, 4)))
     return fail(NVFP4_ERR_INVALID_ARG, "a_row_src and expert_offsets must be 4-byte aligned");
+  const int64_t kb = (K + 127) / 128;
+  if (overlap(c, 2 * M * N, a_q, rows_a * K) || overlap(c, 2 * M * N, a_sf, 4 * rows_a * kb) ||
+      overlap(c, 2 * M * N, b_q, E * N * K) || overlap(c, 2 * M * N, b_sf, 4 * E * ((N + 127) / 128) * kb) ||
+      (a_row_src && overlap(c, 2 * M * N, a_row_src, 4 * M)) ||
+      (expert_offsets && overlap(c, 2 * M * N, expert_offsets, 4 * (int64_t(E) + 1))))
+    return fail(NVFP4_ERR_INVALID_ARG, "c must not overlap the inputs");
   nvfp4_status st = check_arch();
   if (st != NVFP4_OK) return st;
   const nvfp4::Fp8GemmArgs a{a_q, a_sf, rows_a, a_row_src, a_row_div, expert_offsets, E, M, N, K, b_q, b_sf, c};

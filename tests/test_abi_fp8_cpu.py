@@ -38,6 +38,8 @@ def _gemm(**kw):
     (dict(a=None), -1), (dict(asf=None), -1), (dict(b=None), -1), (dict(bsf=None), -1),
     (dict(c=None), -1), (dict(a=P[0] + 8), -1), (dict(b=P[3] + 4), -1), (dict(asf=P[1] + 2), -1),
     (dict(c=P[5] + 1), -1), (dict(off=P[2] + 2), -1), (dict(src=P[6] + 1), -1),
+    (dict(c=P[0] + 64), -1), (dict(c=P[1]), -1), (dict(c=P[3] + 16), -1), (dict(c=P[4]), -1),   # c over an input
+    (dict(src=P[6], c=P[6]), -1), (dict(c=P[2] + 2), -1),
     (dict(M=(1 << 31) - 1, rows=(1 << 31) - 1, N=1 << 20, K=16), -2),   # too many tiles
 ])
 def test_fp8_grouped_gemm_rejects(L, kw, status):
@@ -62,6 +64,10 @@ def test_fp8_quantize_rejects(L, name, two):
                          ((P[0] + 8, 1, 32, 64, None, P[1], P[2]), -1),
                          ((P[0], 1, 32, 64, None, P[1] + 4, P[2]), -1),
                          ((P[0], 1, 32, 64, None, P[1], P[2] + 2), -1),
+                         ((P[0], 1, 32, 64, None, P[0] + 8, P[2]), -1),
+                         ((P[0], 9, 32, 64, None, P[1], P[0] + 1024), -1),
+                         ((P[0], 9, 32, 64, None, P[1], P[1] + 32), -1),
+                         ((P[0], (1 << 31) - 1, 32, (1 << 40) - 8, None, P[1], P[2]), -2),
                          ((P[0], 1, 32, 64, P[3] + 2, P[1], P[2]), -1)]:
         assert f(*args, None) == status, args
         assert L.nvfp4_last_error() != b""
@@ -74,6 +80,7 @@ def test_fp8_quantize_weight_rejects(L):
                          ((P[0], 1, 4, 8, P[1], P[2]), -2), ((P[0], 1, 4, 1 << 24, P[1], P[2]), -2),
                          ((P[0], 1 << 31, 1, 16, P[1], P[2]), -2), ((P[0], 1 << 30, 256, 128, P[1], P[2]), -2),
                          ((None, 1, 4, 16, P[1], P[2]), -1), ((P[0], 1, 4, 16, None, P[2]), -1),
+                         ((P[0], 1, 4, 16, P[0] + 64, P[2]), -1), ((P[0], 1, 4, 16, P[1], P[1] + 8), -1),
                          ((P[0], 1, 4, 16, P[1], None), -1), ((P[0] + 2, 1, 4, 16, P[1], P[2]), -1)]:
         assert f(*args, None) == status, args
     assert f(None, 0, 4, 16, None, None, None) == 0 and f(None, 4, 0, 16, None, None, None) == 0
