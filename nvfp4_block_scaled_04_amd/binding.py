@@ -634,6 +634,8 @@ def _fp8_rows(name, x, C, offsets, out):
     n_rows = None
     if offsets is not None:
         _is(offsets, torch.int32, "offsets")
+        if offsets.numel() < 1:
+            raise ValueError("offsets must hold the row count")
         n_rows = offsets.data_ptr() + 4 * (offsets.numel() - 1)
     ld = x.stride(0) if R > 1 else (x.shape[1] + 7) // 8 * 8   # a one-row tensor's row stride is arbitrary
     _call(name, (x, q, sf, offsets), _ptr(x), R, C, ld, n_rows, _ptr(q), _ptr(sf))

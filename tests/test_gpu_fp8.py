@@ -176,7 +176,7 @@ def _run(counts, N, K, k=1, extra=0, seed=0, special=False, gather=False, bad=Fa
     if gather:
         src = rng.permutation(R * k)[:M].astype(np.int32)
         if bad and M > 3:
-            src[1], src[M // 2] = -k * 5, (R + 3) * k       # indices outside A: rows of zeros
+            src[1], src[2], src[M // 2] = -k * 5, -1, (R + 3) * k       # indices outside A: rows of zeros
         rows = np.where((src // k >= 0) & (src >= 0) & (src // k < R), src // k, -1)
     ref, mag, peak = P.grouped_product(P.decode(a, asf), [P.decode(b[e], bsf[e], 128) for e in range(E)], off, rows)
     da, das, db, dbs = _dev(a, asf, b, bsf)
@@ -327,6 +327,8 @@ def test_binding_refusals():
         nv.fp8_grouped_gemm(ops[0].view(torch.uint8), *ops[1:], offsets=off)
     with pytest.raises(ValueError):
         nv.fp8_grouped_gemm(ops[0], ops[1].t(), *ops[2:], offsets=off)
+    with pytest.raises(ValueError):
+        nv.fp8_quantize(torch.zeros((2, 32), dtype=torch.bfloat16, device=DEV), offsets=off[:0])
     with pytest.raises(nv.Nvfp4Error):
         nv.fp8_quantize(torch.zeros((2, 24), dtype=torch.bfloat16, device=DEV))
     with pytest.raises(ValueError):
