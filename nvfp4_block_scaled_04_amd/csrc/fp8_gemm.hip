@@ -17,6 +17,7 @@
 // stays an order of magnitude below the BF16 rounding of c, and the codes
 // themselves are off by up to 2^-4, so no slower instruction is taken for it.
 #include <atomic>
+#include <cmath>
 
 #include "internal.hpp"
 #include "device.hpp"
@@ -880,9 +881,12 @@ hipError_t device_cus(int& cus) {
 //              58 us with 16 x 64)
 //   tiles      (6 + JV) a round (N 2048: 2048 rows 44 us with 96-row tiles in one
 //              round, 73 us with 288; 4096 rows 88 us with 96-row tiles in
-//              two rounds, 61 us with 128)
+//              two rounds, 61 us with 128), and 12 at least where the weights
+//              are one tile's alone and each stage waits for HBM (8 experts of
+//              14 rows, N 4096: 63 us, streaming 40 us)
 //   streaming  3.2 + B/60 for B workgroups (1 row, N 32768: 36 us; the others
-//              47 us and more)
+//              47 us and more), 1.3 of that for experts of several tiles
+//              (2 experts of 33 rows, N 3473, K 3328: 20 us, 64 x 32 15 us)
 // and none is faster than its experts' weights come from HBM: N * live / 4100
 // units (256 experts, N 4096, 8 rows each: streaming 1.11 ms, tiles 1.19 ms; 16
 // rows each: 1.30 ms, 1.19 ms).
@@ -895,23 +899,29 @@ Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
   const int64_t live = a.E < a.M ? a.E : a.M;
   const double avg = (double)a.M / live;
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-  // m tiles of bm rows; an expert's last one is half full on average
+  // m tiles of bm rows: an expert's last one is half full on average; rows that
+  // spread by the root of their average and still fit one tile are one (25
+  // experts of 53 rows, N 529, K 5984: 64 x 64 a workgroup 29 us, tiles 51 us)
   auto m_tiles = [&](int bm) {
     if (!a.offsets) return (double)up(a.M, bm);
-    const double per = avg / bm + 0.5;
-    return live * (per > 1.0 ? per : 1.0);
+    return live * (avg + std::sqrt(avg) <= bm ? 1.0 : std::fmax(avg / bm + 0.5, 1.0));
   };
   auto rounds = [&](double tiles, int64_t n_tiles) { return (double)(int64_t)((tiles * n_tiles + cus - 1) / cus); };
   const double hbm = (double)live * a.N / 4100.0 * (256.0 / cus);
-  auto over_hbm = [&](double c) { return c > hbm ? c : hbm * 1.02; };
+  auto over_hbm = [&](double c) { return std::fmax(c, hbm * 1.02 + 0.01 * c); };
   const double blocks = m_tiles(16) * up(a.N, kStN) * (256.0 / cus);
   const double first = 3.2 + blocks / 60, flow = m_tiles(16) * a.N / 4400.0 * (256.0 / cus);
-  double cost = first > flow ? first : flow;
+  double cost = (first > flow ? first : flow) * (avg > 16 ? 1.3 : 1.0);
   Fp8Plan best{0, 0, 1, 0};
-  for (int bm = kTlM; bm >= kTlMin; bm -= 32) {
-    const double tiles = m_tiles(bm);
+  for (int bm = kTlMin; bm <= kTlM; bm += 32) {
+    const double tiles = m_tiles(bm), wgs = tiles * up(a.N, kTlN), r = rounds(tiles, up(a.N, kTlN));
     const double jv = (double)up((int64_t)(a.M / tiles + 0.999), 32);
-    const double c = over_hbm(rounds(tiles, up(a.N, kTlN)) * (6.0 + (jv > 3.0 ? jv : 3.0)));
+    const double stages = std::fmax(6.0 + std::fmax(jv, 3.0), tiles < 2 * live ? 12.0 : 0.0);
+    // Experts above the average: in a round that is nearly full their further
+    // tiles start another one, so high tiles (16 experts of 116 rows, N 4096,
+    // K 2048: 35 us with 288, 48 us with 128); else they fill idle CUs, so low ones.
+    const bool full = a.offsets && wgs > (r - 0.25) * cus;
+    const double c = over_hbm(r * stages * (full && r < 4 ? 1.1 : 1.0)) + (full ? kTlM - bm : bm) * 1e-5;
     if (c < cost) { cost = c; best = Fp8Plan{2, 0, 0, bm}; }
   }
   static const int kShape[6][2] = {{1, 1}, {2, 1}, {4, 1}, {2, 2}, {4, 2}, {4, 4}};
