@@ -244,6 +244,20 @@ def test_product_dense_tiles(jv, N, K):
     _check(c, ref, mag, peak, K, M)
 
 
+@pytest.mark.parametrize("N,shift", [(65, 0), (70, 0), (258, 0), (72, 1), (72, 2), (3, 1), (62, 2)])
+def test_product_tile_widths_and_places(N, shift):
+    """Rows at 2-, 4- and 16-byte places; nothing before or behind them is written."""
+    M, K = 256 * 96 - 5, 144
+    print(f"[case] fp8 tile widths N={N} shift={shift}", flush=True)
+    a, asf, b, bsf = _operands(np.random.default_rng(N), M, 1, N, K)
+    buf = torch.full((M * N + 16,), 3.0, dtype=torch.bfloat16, device=DEV)
+    c = buf[8 + shift:8 + shift + M * N].view(M, N)
+    nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf), out=c)
+    ref, mag, peak = P.grouped_product(P.decode(a, asf), [P.decode(b[0], bsf[0], 128)], [0, M], np.arange(M))
+    _check(c, ref, mag, peak, K, M)
+    assert torch.all(buf[:8 + shift] == 3) and torch.all(buf[8 + shift + M * N:] == 3)
+
+
 @pytest.mark.parametrize("K", [128, 144, 384, 512, 1040, 1168])
 def test_product_grouped_tiles(K):
     rng = np.random.default_rng(K)
@@ -267,6 +281,13 @@ def test_product_few_rows_shapes(M, N, K):
     c = nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf))
     ref, mag, peak = P.grouped_product(P.decode(a, asf), [P.decode(b[0], bsf[0], 128)], [0, M], np.arange(M))
     _check(c, ref, mag, peak, K, M)
+
+
+@pytest.mark.parametrize("counts,N,K", [([53, 61, 0, 64, 40] * 5, 529, 272), ([33, 20], 1735, 400), ([31, 32, 27, 9], 1030, 528),
+                                        ([14, 1, 0, 16], 2050, 144), ([70, 90, 100, 30], 1030, 400), ([10, 15, 9] * 6, 129, 1040)],
+                         ids=lambda v: f"{len(v)}x{sum(v)}" if isinstance(v, list) else str(v))
+def test_product_few_rows_an_expert(counts, N, K):
+    _run(counts, N, K, k=2, extra=3, gather=True, bad=True, special=True)
 
 
 def test_product_layer_shape_against_sampled_columns():
