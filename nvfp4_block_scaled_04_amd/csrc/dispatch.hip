@@ -169,6 +169,10 @@ __global__ __launch_bounds__(TPT >= kGroupThreads ? TPT : kGroupThreads) void co
           dot[b] += s;
         }
       }
+      // no row: 0 also where dout is not finite
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (d[b] < 0 || d[b] >= n) dot[b] = 0.0f;
     }
     if (!dw) continue;
 #pragma unroll

@@ -66,6 +66,25 @@ def test_dispatch_and_gradients(T, k, E, H, bad):
     assert none is None and torch.equal(only.view(torch.int16), dy.view(torch.int16))
 
 
+@pytest.mark.parametrize("k,H", [(3, 64), (9, 1000), (4, 2056)])
+def test_combine_gradient_of_non_finite_rows(k, H):
+    """dout of infinities and NaN: dy and dw of pairs with an invalid expert id
+    stay zero, and other tokens' stay finite."""
+    T, E = 20, 5
+    rng = np.random.default_rng(H)
+    ids, off, _, inv = _routing(rng, T, k, E, 0.3)
+    dout, y = _bf(rng, T, H), _bf(rng, T * k, H)
+    dout[::3, 1], dout[1::3, H - 1] = float("inf"), float("nan")
+    w = torch.from_numpy(rng.random((T, k)).astype(np.float32) + 0.5)
+    dy, dw = nv.moe_combine_bwd(dout.to(DEV), y.to(DEV), inv, w.to(DEV), off)
+    bad = host(inv).reshape(T, k) >= int(off[-1])
+    assert np.array_equal(bad, ids < 0) and bad.any()
+    got, dy = host(dw), bf16_values(host(dy))
+    assert np.all(got[bad] == 0) and np.all(dy[int(off[-1]):] == 0)
+    finite = np.isfinite(dout.float().numpy()).all(1)
+    assert np.isfinite(got[finite]).all() and not np.isfinite(got[~finite][~bad[~finite]]).any()
+
+
 def test_outputs_stay_inside_their_buffers():
     rng = np.random.default_rng(3)
     for T, k, H in [(5, 3, 24), (3, 2, 1000), (2, 8, 7168)]:
