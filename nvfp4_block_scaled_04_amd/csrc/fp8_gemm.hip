@@ -81,7 +81,7 @@ __device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, 
   t.row0 = (int64_t)first + at;
   if (t.row0 + left > p.M) left = (int)(p.M - t.row0);
   t.nrows = left;
-  return left > 0;
+  return left > 0 && t.row0 >= 0;
 }
 
 // Wave-wide sum of v over the lanes up to this one.
