@@ -674,8 +674,9 @@ nvfp4_status fp8_rows_impl(bool swiglu, const char* what, const void* x, int64_t
   if (!aligned(x, 16) || !aligned(q, 8) || !aligned(sf, 4) || (n_rows && !aligned(n_rows, 4)))
     return fail(NVFP4_ERR_INVALID_ARG, "x must be 16-byte, q 8-byte, sf and n_rows 4-byte aligned");
   const int64_t xb = 2 * ((rows - 1) * ld_x + width), qb = rows * cols, sb = 4 * rows * ((cols + 127) / 128);
-  if (overlap(q, qb, x, xb) || overlap(sf, sb, x, xb) || overlap(q, qb, sf, sb))
-    return fail(NVFP4_ERR_INVALID_ARG, "q and sf must not overlap x or each other");
+  if (overlap(q, qb, x, xb) || overlap(sf, sb, x, xb) || overlap(q, qb, sf, sb) ||
+      (n_rows && (overlap(q, qb, n_rows, 4) || overlap(sf, sb, n_rows, 4))))
+    return fail(NVFP4_ERR_INVALID_ARG, "q and sf must not overlap the inputs or each other");
   nvfp4_status st = check_arch();
   if (st != NVFP4_OK) return st;
   return finish(nvfp4::launch_fp8_rows(swiglu, x, rows, cols, ld_x, n_rows, q, sf,
@@ -714,8 +715,11 @@ nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* inv_perm, const in
   if (T == 0) return NVFP4_OK;
   if (!x || !inv_perm || !off || !rows)
     return fail(NVFP4_ERR_INVALID_ARG, "x, inv_perm, expert_offsets and rows must be non-NULL");
-  if (!aligned(x, 16) || !aligned(rows, 16)) return fail(NVFP4_ERR_INVALID_ARG, "x and rows must be 16-byte aligned");
-  if (overlap(rows, 2 * T * k * H, x, 2 * T * H)) return fail(NVFP4_ERR_INVALID_ARG, "rows must not overlap x");
+  if (!aligned(x, 16) || !aligned(rows, 16) || !aligned(inv_perm, 4) || !aligned(off, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "x and rows must be 16-byte, inv_perm and expert_offsets 4-byte aligned");
+  const int64_t n = 2 * T * k * H;
+  if (overlap(rows, n, x, 2 * T * H) || overlap(rows, n, inv_perm, 4 * T * k) || overlap(rows, n, off + E, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "rows must not overlap the inputs");
   st = check_arch();
   if (st != NVFP4_OK) return st;
   return finish(nvfp4::launch_dispatch(x, inv_perm, off, T, k, E, H, rows, static_cast<hipStream_t>(stream)),
@@ -729,8 +733,11 @@ nvfp4_status nvfp4_moe_dispatch_bwd(const void* drows, const int32_t* inv_perm, 
   if (T == 0) return NVFP4_OK;
   if (!drows || !inv_perm || !off || !dx)
     return fail(NVFP4_ERR_INVALID_ARG, "drows, inv_perm, expert_offsets and dx must be non-NULL");
-  if (!aligned(drows, 16) || !aligned(dx, 16)) return fail(NVFP4_ERR_INVALID_ARG, "drows and dx must be 16-byte aligned");
-  if (overlap(dx, 2 * T * H, drows, 2 * T * k * H)) return fail(NVFP4_ERR_INVALID_ARG, "dx must not overlap drows");
+  if (!aligned(drows, 16) || !aligned(dx, 16) || !aligned(inv_perm, 4) || !aligned(off, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "drows and dx must be 16-byte, inv_perm and expert_offsets 4-byte aligned");
+  const int64_t n = 2 * T * H;
+  if (overlap(dx, n, drows, 2 * T * k * H) || overlap(dx, n, inv_perm, 4 * T * k) || overlap(dx, n, off + E, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "dx must not overlap the inputs");
   st = check_arch();
   if (st != NVFP4_OK) return st;
   return finish(nvfp4::launch_dispatch_bwd(drows, inv_perm, off, T, k, E, H, dx, static_cast<hipStream_t>(stream)),
@@ -745,10 +752,13 @@ nvfp4_status nvfp4_moe_combine_bwd(const void* dout, const void* y, const int32_
   if (T == 0) return NVFP4_OK;
   if (!dout || !inv_perm || !topk_w || !off || !dy || (dw && !y))
     return fail(NVFP4_ERR_INVALID_ARG, "dout, inv_perm, topk_w, expert_offsets, dy and (with dw) y must be non-NULL");
-  if (!aligned(dout, 16) || !aligned(dy, 16) || (dw && !aligned(y, 16)) || !aligned(dw, 4))
-    return fail(NVFP4_ERR_INVALID_ARG, "dout, y and dy must be 16-byte and dw 4-byte aligned");
+  if (!aligned(dout, 16) || !aligned(dy, 16) || (dw && !aligned(y, 16)) || !aligned(dw, 4) ||
+      !aligned(inv_perm, 4) || !aligned(topk_w, 4) || !aligned(off, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "dout, y and dy must be 16-byte, the other arrays 4-byte aligned");
   const int64_t rows = 2 * T * k * H;
   if (overlap(dy, rows, dout, 2 * T * H) || overlap(dy, rows, topk_w, 4 * T * k) ||
+      overlap(dy, rows, inv_perm, 4 * T * k) || overlap(dy, rows, off + E, 4) ||
+      (dw && (overlap(dw, 4 * T * k, inv_perm, 4 * T * k) || overlap(dw, 4 * T * k, off + E, 4))) ||
       (dw && (overlap(dy, rows, y, rows) || overlap(dy, rows, dw, 4 * T * k) ||
               overlap(dw, 4 * T * k, topk_w, 4 * T * k) || overlap(dw, 4 * T * k, dout, 2 * T * H) ||
               overlap(dw, 4 * T * k, y, rows))))

@@ -46,7 +46,7 @@ template <int TPT>
 __device__ __forceinline__ int64_t my_token(int& tid) {
   constexpr int per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT;
   tid = threadIdx.x % TPT;
-  return (int64_t)blockIdx.x * per + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
+  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * per + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
 }
 
 // Reads of a token's slots through the constant address space: scalar loads,
@@ -215,10 +215,11 @@ void by_width(int hv, A&&... a) {
   else F<896>::go(a...);
 }
 
+// in rows of workgroups, since one row holds fewer than 2^32 threads
 template <int TPT>
-unsigned grid_of(int64_t T) {
-  const int per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT;
-  return (unsigned)((T + per - 1) / per);
+dim3 grid_of(int64_t T) {
+  const int64_t per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT, n = (T + per - 1) / per, row = 1 << 20;
+  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
 }
 template <int TPT>
 constexpr int threads_of() { return TPT >= kGroupThreads ? TPT : kGroupThreads; }

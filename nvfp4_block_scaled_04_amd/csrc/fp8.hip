@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
     const int64_t n = n_rows[0];
     rows = n < rows ? n : rows;
   }
-  const uint32_t unit = blockIdx.x * kQGroups + (threadIdx.x >> 4);
+  const uint32_t unit = (blockIdx.y * gridDim.x + blockIdx.x) * kQGroups + (threadIdx.x >> 4);
   const uint32_t chunk = unit / (uint32_t)kblocks;
   const int kb = (int)(unit - chunk * (uint32_t)kblocks);
   const int64_t row0 = (int64_t)chunk * ROWS;
@@ -166,7 +166,9 @@ template <bool SWIGLU, int ROWS>
 static void rows_launch(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int kblocks,
                         const int32_t* n_rows, uint8_t* q, float* sf, hipStream_t stream) {
   const int64_t units = (rows + ROWS - 1) / ROWS * kblocks;
-  const unsigned grid = (unsigned)((units + kQGroups - 1) / kQGroups);
+  // in rows of workgroups, since one row holds fewer than 2^32 threads
+  const int64_t n = (units + kQGroups - 1) / kQGroups, row = 1 << 20;
+  const dim3 grid = n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
   fp8_rows_kernel<SWIGLU, ROWS><<<grid, kQThreads, 0, stream>>>(
       static_cast<const uint16_t*>(x), rows, (int)cols, ld_x, kblocks, n_rows, q, sf);
 }

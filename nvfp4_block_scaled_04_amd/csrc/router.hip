@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __r
                                                               float* __restrict__ dlogits) {
 #pragma clang fp contract(off)   // else w * g would round differently lane by lane in the exchanges
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (t >= T) return;                          // the whole wave
   float w = 0.0f, g = 0.0f;
   int id = -1;
@@ -135,7 +135,9 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __r
 hipError_t launch_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
                                   int64_t T, int E, int k, float* dlogits, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)((T + 3) / 4);
+  // in rows of workgroups, since one row holds fewer than 2^32 threads
+  const int64_t n = (T + 3) / 4, row = 1 << 20;
+  const dim3 blocks = n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
   // 16-byte stores where every row starts on a 16-byte boundary
   if (E % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0)
     router_topk_bwd_kernel<true><<<blocks, 256, 0, stream>>>(topk_ids, topk_w, dw, T, E, k, dlogits);

@@ -68,6 +68,7 @@ def test_fp8_quantize_rejects(L, name, two):
                          ((P[0], 9, 32, 64, None, P[1], P[0] + 1024), -1),
                          ((P[0], 9, 32, 64, None, P[1], P[1] + 32), -1),
                          ((P[0], (1 << 31) - 1, 32, (1 << 40) - 8, None, P[1], P[2]), -2),
+                         ((P[0], 1, 32, 64, P[1], P[1], P[2]), -1), ((P[0], 1, 32, 64, P[2], P[1], P[2]), -1),
                          ((P[0], 1, 32, 64, P[3] + 2, P[1], P[2]), -1)]:
         assert f(*args, None) == status, args
         assert L.nvfp4_last_error() != b""
@@ -102,6 +103,12 @@ def test_dispatch_and_gradients_reject(L):
     assert L.nvfp4_moe_dispatch(P[0], P[1], P[2], *good, P[0] + 112, None) == -1       # x is 128 bytes
     assert L.nvfp4_moe_dispatch(P[0], P[1], P[2], *good, P[0] - 16, None) == -1
     assert L.nvfp4_moe_dispatch_bwd(P[9], P[1], P[2], *good, P[9] + 16, None) == -1
+    for bad in ((P[1] + 2, P[2]), (P[1], P[2] + 2), (P[9], P[2]), (P[1], P[9])):         # misaligned, or over an output
+        assert L.nvfp4_moe_dispatch(P[0], *bad, *good, P[9], None) == -1
+        assert L.nvfp4_moe_dispatch_bwd(P[0], *bad, *good, P[9], None) == -1
+        assert L.nvfp4_moe_combine_bwd(P[0], P[8], bad[0], P[3], bad[1], *good, P[9], P[4], None) == -1
+    assert L.nvfp4_moe_combine_bwd(P[0], P[8], P[4], P[3], P[2], *good, P[9], P[4], None) == -1
+    assert L.nvfp4_moe_combine_bwd(P[0], P[8], P[1], P[3] + 2, P[2], *good, P[9], P[4], None) == -1
     for i in (0, 1, 2, 3, 4, 5):
         ptr = [P[0], P[9], P[1], P[3], P[2], P[8]]
         ptr[i] = None

@@ -85,6 +85,30 @@ def test_combine_gradient_of_non_finite_rows(k, H):
     assert np.isfinite(got[finite]).all() and not np.isfinite(got[~finite][~bad[~finite]]).any()
 
 
+def test_more_tokens_than_a_row_of_workgroups():
+    """2^26 + 5 tokens of eight columns: more threads than 2^32."""
+    T = (1 << 26) + 5
+    perm = torch.randperm(T, device=DEV)
+    inv = torch.empty(T, dtype=torch.int32, device=DEV)
+    inv[perm] = torch.arange(T, dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, T - 3], dtype=torch.int32, device=DEV)
+    x = torch.arange(T * 8, dtype=torch.int32, device=DEV).bitwise_and_(0x3F7F).to(torch.int16).view(torch.bfloat16).view(T, 8)
+    rows = nv.moe_dispatch(x, inv, off, 1)
+    want = torch.cat([x[p] for p in perm.split(1 << 24)])   # indexed at once it comes out wrong at this size
+    want[T - 3:] = 0
+    assert torch.equal(rows.view(torch.int16), want.view(torch.int16))
+    back = nv.moe_dispatch_bwd(rows, inv, off, 1)
+    kept = torch.where((inv < T - 3)[:, None], x, torch.zeros_like(x))
+    assert torch.equal(back.view(torch.int16), kept.view(torch.int16))
+    del want, kept, back
+    w = torch.full((T, 1), 0.5, device=DEV)
+    dy, _ = nv.moe_combine_bwd(x, None, inv, w, off, need_dw=False)
+    assert torch.equal(dy, rows * 0.5)
+    ids, dw = torch.zeros((T, 1), dtype=torch.int32, device=DEV), torch.ones((T, 1), device=DEV)
+    dl = nv.router_topk_bwd(ids, w, dw, 1)
+    assert torch.all(dl == 0.25)                         # 0.5 * (1 - 0.5 * 1)
+
+
 def test_outputs_stay_inside_their_buffers():
     rng = np.random.default_rng(3)
     for T, k, H in [(5, 3, 24), (3, 2, 1000), (2, 8, 7168)]:
