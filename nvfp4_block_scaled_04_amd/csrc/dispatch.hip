@@ -11,7 +11,7 @@
 // and each token row is read once for its k expert rows.  All are bound by
 // HBM (16-byte vectors, kBatch rows in flight per thread).  Measured with 8192
 // tokens x 8 rows of 7168: dispatch 184 us and its gradient 182 us (1.06 GB:
-// 5.8 TB/s), combine's gradient 350 to 400 us (2.0 GB: 5.0 to
+// 5.8 TB/s), combine's gradient 350 to 405 us (2.0 GB: 4.9 to
 // 5.7 TB/s); a large copy reaches 4.9 TB/s.  256 tokens: dispatch 6.6 us.
 #include "internal.hpp"
 #include "device.hpp"
