@@ -477,8 +477,8 @@ nvfp4_status nvfp4_moe_combine_bwd(const void* dout_bf16, const void* y_bf16,
  *
  * nvfp4_fp8_quantize: v = x[row][col], row r at x + r*ld_x elements.
  * nvfp4_fp8_swiglu_quantize: x rows hold [gate | up], cols columns each;
- *   v = gate / (1 + exp(-gate)) * up in fp32 (not rounded to BF16), q has cols
- *   columns.  The step between the two products of an FP8 expert.
+ *   v = gate / (1 + exp(-gate)) * up in fp32, within 2^-21 of itself (not
+ *   rounded to BF16), q has cols columns.  The step between the two products of an FP8 expert.
  *   n_rows (nullable, device int32[1], e.g. expert_offsets + E): rows >=
  *   n_rows[0] are neither read nor written.
  * nvfp4_fp8_quantize_weight: groups matrices [N][K], contiguous.

@@ -12,9 +12,8 @@
 // element, SwiGLU reads 4, weights read 2 and write 1.  Sixteen lanes hold
 // one 128-column block, 16 bytes (8 BF16) each, so its maximum is four lane
 // exchanges and nothing is read twice.  Measured: 8192 rows of 7168 29 us
-// (178 MB: 6.1 TB/s); SwiGLU of 65536 x 2048 148 us (4.6 TB/s: the exp and
-// the division of each element cost beside the loads), of 2048 x 2048 7.6 us
-// (latency); weights 32 x 4096 x 7168 517 us (2.8 GB: 5.4 TB/s).
+// (178 MB: 6.1 TB/s); SwiGLU of 65536 x 2048 126 us (5.4 TB/s), of
+// 2048 x 2048 6.2 us (latency); weights 32 x 4096 x 7168 517 us (2.8 GB: 5.4 TB/s).
 #include "internal.hpp"
 #include "device.hpp"
 
@@ -60,18 +59,28 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float r) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// silu(g) * u with every step rounded (no contraction): the same bits as the
-// formula g / (1 + exp(-g)) * u written out in fp32
-__device__ __forceinline__ void swiglu8(const uint4& gv, const uint4& uv, float (&h)[8]) {
+// silu(g) * u = (g / 4) / ((1 + exp(-g)) / 4) * u within 2^-21 of itself, far
+// below the codes' 2^-4.  exp(-g) is 2^t times 1 + lo ln 2 with t + lo = -g log2 e
+// (lo: what t's rounding and the constant's leave); the quarter keeps the
+// reciprocal a normal number up to the largest finite exp(-g).  g beyond +-100
+// gives g or 0, -inf and NaN give NaN, as the formula does.  The hardware's exp2
+// and reciprocal (2^-23 each) without the library's exp and a full division,
+// half the instructions, which bound large calls (65536 x 2048: 148 us with them, 129 without).
+__device__ __forceinline__ float swiglu(float g, float u) {
 #pragma clang fp contract(off)
+  constexpr float kLog2e = 1.44269502e+00f, kLog2eLo = 1.92596299e-08f, kLn2 = 0.693147181f;
+  const float c = __builtin_amdgcn_fmed3f(g, -100.0f, 100.0f);
+  const float t = c * -kLog2e;
+  const float lo = fmaf(c, -kLog2eLo, fmaf(c, -kLog2e, -t));
+  const float d = fmaf(__builtin_amdgcn_exp2f(t), fmaf(lo, 0.25f * kLn2, 0.25f), 0.25f);
+  return 0.25f * g * __builtin_amdgcn_rcpf(d) * u;
+}
+__device__ __forceinline__ void swiglu8(const uint4& gv, const uint4& uv, float (&h)[8]) {
   float g[8], u[8];
   unpack8(gv, g);
   unpack8(uv, u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = g[i] / (1.0f + expf(-g[i]));
-    h[i] = s * u[i];
-  }
+  for (int i = 0; i < 8; ++i) h[i] = swiglu(g[i], u[i]);
 }
 
 // One lane group per (ROWS rows, 128-column block).  SWIGLU: x rows hold
@@ -177,16 +186,13 @@ hipError_t launch_fp8_rows(bool swiglu, const void* x, int64_t rows, int64_t col
                            const int32_t* n_rows, uint8_t* q, float* sf, hipStream_t stream) {
   if (rows == 0) return hipSuccess;
   const int kblocks = (int)((cols + 127) / 128);
-  // four rows a lane group where that still gives every CU several workgroups
-  // (8192 x 7168: 29 us, one row 32 us; SwiGLU 2048 x 2048: 9.1 us, one row 7.4 us)
-  const bool few = rows * kblocks < (1 << 16);
-  if (swiglu) {
-    if (few) rows_launch<true, 1>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
-    else rows_launch<true, 4>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
-  } else {
-    if (few) rows_launch<false, 1>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
-    else rows_launch<false, 4>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
-  }
+  // rows: four a lane group where that still gives every CU several workgroups
+  // (8192 x 7168: 29.7 us, one row 32.7; 1024 x 7168: 6.8, one row 6.3).  SwiGLU
+  // loads twice as much a row: one (65536 x 2048: 126 us, four rows 129; 2048 x
+  // 2048: 6.2, four rows 7.7).
+  if (swiglu) rows_launch<true, 1>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
+  else if (rows * kblocks < (1 << 16)) rows_launch<false, 1>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
+  else rows_launch<false, 4>(x, rows, cols, ld_x, kblocks, n_rows, q, sf, stream);
   return hipGetLastError();
 }
 

@@ -123,6 +123,27 @@ def test_swiglu_quantize(R, I):
     _check_swiglu(x, q, sf)
 
 
+def test_swiglu_of_every_bf16_gate():
+    """One gate a row, up 1: the row's scale is |silu| / 448.  exp2 and the
+    reciprocal within an ulp (2^-23 each), four roundings of 2^-24 on the way to
+    silu and two of the scale: 2^-21 + 2^-23 relative, down to the floor of
+    2^-100; one sign's infinity and NaN give NaN codes."""
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16)
+    x = torch.zeros((1 << 16, 32), dtype=torch.bfloat16)
+    x[:, 0] = bits.view(torch.bfloat16)
+    x[:, 16] = 1
+    q, sf = nv.fp8_swiglu_quantize(x.to(DEV))
+    g = x[:, 0].double().numpy()
+    with np.errstate(over="ignore", invalid="ignore"):
+        h = g / (1 + np.exp(-g))
+    got, code = host(sf)[:, 0].astype(np.float64), _codes(q)
+    ok = np.isfinite(h)
+    want = np.maximum(np.abs(h[ok]), 2.0 ** -100) / 448
+    assert np.all(np.abs(got[ok] - want) <= want * (2.0 ** -21 + 2.0 ** -23))
+    assert np.array_equal(code[ok, 0] >= 0x80, np.signbit(g[ok]))
+    assert np.all(code[~ok, 0] & 0x7F == 0x7F) and np.all(code[:, 1:] == 0)
+
+
 def test_swiglu_row_count_leaves_the_rest():
     x = _acts(np.random.default_rng(8), 9, 64).to(DEV)
     ref, rs = nv.fp8_swiglu_quantize(x)
