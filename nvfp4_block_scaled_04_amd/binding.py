@@ -612,7 +612,8 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
         raise ValueError("dout and topk_w must be 2-D")
     T, H = dout.shape
     k = topk_w.shape[1]
-    _is(topk_w, torch.float32, "topk_w", (T, k))
+    if topk_w.shape[0] != T:
+        raise ValueError(f"topk_w must have shape {(T, k)} (got {tuple(topk_w.shape)})")
     if need_dw:
         _is(y, torch.bfloat16, "y", (T * k, H))
     _is(inv_perm, torch.int32, "inv_perm", (T * k,))
@@ -624,6 +625,13 @@ def moe_combine_bwd(dout, y, inv_perm, topk_w, offsets, out=None, need_dw=True):
           _ptr(dout), _ptr(y) if need_dw else None, _ptr(inv_perm), _ptr(topk_w), _ptr(offsets), T, k,
           offsets.numel() - 1, H, _ptr(dy), _ptr(dw))
     return dy, dw
+
+
+def _is_rows(x):
+    """_dev(rows=True) of a BF16 x, with the usual case first."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is torch.bfloat16 and x.dim() == 2
+            and x.is_contiguous()):
+        _dev(x, torch.bfloat16, "x", rows=True)
 
 
 def _fp8_rows(name, x, C, offsets, out):
@@ -646,14 +654,14 @@ def fp8_quantize(x, offsets=None, out=None):
     """x (R, C) bf16 -> FP8 codes q (R, C) float8_e4m3fn and one float32 scale
     per 128 columns of a row, sf (R, ceil(C/128)).  x's rows may be spaced apart.
     offsets (expert offsets): rows from offsets[-1] on are left as they were."""
-    _dev(x, torch.bfloat16, "x", rows=True)
+    _is_rows(x)
     return _fp8_rows("nvfp4_fp8_quantize", x, x.shape[1], offsets, out)
 
 
 def fp8_swiglu_quantize(x, offsets=None, out=None):
     """x (R, 2I) bf16 holding [gate | up] -> silu(gate) * up as FP8: codes q
     (R, I) and scales sf (R, ceil(I/128)), as fp8_quantize makes them."""
-    _dev(x, torch.bfloat16, "x", rows=True)
+    _is_rows(x)
     if x.shape[1] % 2:
         raise ValueError("x must hold [gate | up]: an even number of columns")
     return _fp8_rows("nvfp4_fp8_swiglu_quantize", x, x.shape[1] // 2, offsets, out)

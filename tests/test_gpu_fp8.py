@@ -96,8 +96,8 @@ def test_quantize_weight_bit_exact(G, N, K):
 
 
 def _check_swiglu(x, q, sf):
-    """h = g / (1 + exp(-g)) * u in fp32 against float64: exp and the division
-    within 2 ulp, the sum and the product half an ulp each, so 2^-21 relative
+    """h = g / (1 + exp(-g)) * u in fp32 against float64: exp2 and the reciprocal
+    within an ulp (2^-23 each), four roundings of 2^-24 between, so 2^-21 relative
     covers h; the scale adds 2^-24.  A code then stands for h up to half its
     step, plus that error of h (a value within it of a midpoint may go either
     way)."""
