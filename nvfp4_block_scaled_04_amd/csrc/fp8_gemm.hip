@@ -68,14 +68,15 @@ struct RowTile {
   int64_t row0;
 };
 
-// Tile i of the tiles of at most bm rows that `rows` rows from `first` on are
-// cut into.  The tiles take even shares of the 32-row blocks: 300 rows are
+// Tile i of the tiles of at most bm rows that `rows` (> 0) rows from `first` on
+// are cut into.  Up to 2^31 - 1 rows, so sizes are rounded up without a sum that
+// passes them.  The tiles take even shares of the 32-row blocks: 300 rows are
 // 160 and 140, not 288 and 12, whose second tile would stream the whole
 // weight tile for a twelfth of the work.
-__device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, int rows, int i, RowTile& t) {
+__host__ __device__ __forceinline__ bool cut_tile(const Fp8Params& p, int bm, int first, int rows, int i, RowTile& t) {
   const int unit = bm % 32 ? bm : 32;
-  const int n = (rows + bm - 1) / bm;
-  const int units = (rows + unit - 1) / unit, per = units / n, more = units - per * n;
+  const int n = (rows - 1) / bm + 1;
+  const int units = (rows - 1) / unit + 1, per = units / n, more = units - per * n;
   const int at = (per * i + (i < more ? i : more)) * unit, size = (per + (i < more ? 1 : 0)) * unit;
   int left = rows - at < size ? rows - at : size;
   t.row0 = (int64_t)first + at;
@@ -102,8 +103,8 @@ __device__ __forceinline__ int scan64(int v) {
 struct TileList {
   int S, incl, own;
 
-  __device__ __forceinline__ static int tiles(int lo, int hi, int bm) {
-    return hi > lo ? (hi - lo + bm - 1) / bm : 0;
+  __host__ __device__ __forceinline__ static int tiles(int lo, int hi, int bm) {
+    return hi > lo ? (hi - lo - 1) / bm + 1 : 0;
   }
   __device__ __forceinline__ int count(const Fp8Params& p, int bm) {
     if (!p.offsets) return (int)((p.M + bm - 1) / bm);
@@ -945,6 +946,17 @@ Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
 }
 
 }  // namespace
+
+// The device's cut of expert rows [lo, hi), on the host for the tests: the
+// number of tiles of at most bm rows, and tile i (0 rows if there is none).
+extern "C" int nvfp4_internal_fp8_cut(int64_t M, int lo, int hi, int bm, int i, int64_t* row0, int* nrows) {
+  Fp8Params p{};
+  p.M = M;
+  RowTile t{};
+  *nrows = cut_tile(p, bm, lo, hi - lo, i, t) ? t.nrows : 0;
+  *row0 = t.row0;
+  return TileList::tiles(lo, hi, bm);
+}
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   Fp8Params p;

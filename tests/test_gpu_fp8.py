@@ -440,3 +440,28 @@ def test_product_bad_row_stays_its_own(counts, K):
         assert np.isfinite(got[good]).all() and not np.isfinite(got[~good]).any()
         sums = (128 + 2 + K // 128 + 9) * 2.0 ** -23 * mag + 7 * 2.0 ** -13 * peak
         assert np.all((np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * sums)[good])
+
+
+def _ones(R, K):
+    """(R, K) codes of 1.0, made in pieces: R * K may pass 2^32."""
+    q = torch.empty((R, K), dtype=torch.uint8, device=DEV)
+    for part in q.split(1 << 26):
+        part.fill_(0x38)
+    return q.view(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_product_of_nearly_two_to_the_31_rows(grouped):
+    """2^31 - 100 rows, one column: row d is 16 times its scale, 1 .. 7 in turn
+    (52 GB of operands and output)."""
+    M = (1 << 31) - 100
+    print(f"[case] fp8 rows M={M} grouped={grouped}", flush=True)
+    a, asf = _ones(M, 16), torch.empty((M, 1), device=DEV)
+    for i, part in enumerate(asf.view(-1).split(1 << 26)):
+        part.copy_((torch.arange(len(part), device=DEV) + (i << 26)) % 7 + 1)
+    c = torch.zeros((M + 8, 1), dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV) if grouped else None
+    nv.fp8_grouped_gemm(a, asf, _ones(1, 16)[None], torch.ones((1, 1, 1), device=DEV), offsets=off, out=c[:M])
+    for got, s in zip(c[:M].view(-1).split(1 << 26), asf.view(-1).split(1 << 26)):
+        assert torch.equal(got, (16 * s).to(torch.bfloat16))
+    assert torch.all(c[M:] == 0)
