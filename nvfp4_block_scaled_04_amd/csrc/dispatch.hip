@@ -215,11 +215,10 @@ void by_width(int hv, A&&... a) {
   else F<896>::go(a...);
 }
 
-// in rows of workgroups, since one row holds fewer than 2^32 threads
 template <int TPT>
 dim3 grid_of(int64_t T) {
-  const int64_t per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT, n = (T + per - 1) / per, row = 1 << 20;
-  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
+  constexpr int64_t per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT;
+  return grid_rows((T + per - 1) / per);
 }
 template <int TPT>
 constexpr int threads_of() { return TPT >= kGroupThreads ? TPT : kGroupThreads; }

@@ -126,9 +126,10 @@ __global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
 
 // One workgroup per 128 x 128 block: 16 rows per pass, eight passes in registers.
 __global__ __launch_bounds__(kQThreads) void fp8_weight_kernel(
-    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks,
+    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks, uint32_t units,
     uint8_t* __restrict__ q, float* __restrict__ sf) {
-  const uint32_t unit = blockIdx.x;
+  const uint32_t unit = blockIdx.y * gridDim.x + blockIdx.x;
+  if (unit >= units) return;
   const uint32_t t = unit / (uint32_t)kblocks;
   const int kb = (int)(unit - t * (uint32_t)kblocks);
   const uint32_t g = t / (uint32_t)nblocks;
@@ -175,10 +176,7 @@ template <bool SWIGLU, int ROWS>
 static void rows_launch(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int kblocks,
                         const int32_t* n_rows, uint8_t* q, float* sf, hipStream_t stream) {
   const int64_t units = (rows + ROWS - 1) / ROWS * kblocks;
-  // in rows of workgroups, since one row holds fewer than 2^32 threads
-  const int64_t n = (units + kQGroups - 1) / kQGroups, row = 1 << 20;
-  const dim3 grid = n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
-  fp8_rows_kernel<SWIGLU, ROWS><<<grid, kQThreads, 0, stream>>>(
+  fp8_rows_kernel<SWIGLU, ROWS><<<grid_rows((units + kQGroups - 1) / kQGroups), kQThreads, 0, stream>>>(
       static_cast<const uint16_t*>(x), rows, (int)cols, ld_x, kblocks, n_rows, q, sf);
 }
 
@@ -200,9 +198,9 @@ hipError_t launch_fp8_weight(const void* w, int64_t groups, int64_t rows, int64_
                              float* sf, hipStream_t stream) {
   if (groups == 0 || rows == 0) return hipSuccess;
   const int nblocks = (int)((rows + 127) / 128), kblocks = (int)((cols + 127) / 128);
-  const unsigned grid = (unsigned)(groups * nblocks * kblocks);
-  fp8_weight_kernel<<<grid, kQThreads, 0, stream>>>(static_cast<const uint16_t*>(w), rows, cols, nblocks,
-                                                    kblocks, q, sf);
+  const int64_t units = groups * nblocks * kblocks;
+  fp8_weight_kernel<<<grid_rows(units), kQThreads, 0, stream>>>(static_cast<const uint16_t*>(w), rows, cols, nblocks,
+                                                                kblocks, (uint32_t)units, q, sf);
   return hipGetLastError();
 }
 

@@ -10,6 +10,14 @@
 
 namespace nvfp4 {
 
+// Grid of n (< 2^31) workgroups of up to 1024 threads in rows of 2^20: one row
+// of 2^32 threads or more would wrap without an error.  A kernel's workgroup is
+// blockIdx.y * gridDim.x + blockIdx.x, and those behind the n-th have no work.
+inline dim3 grid_rows(int64_t n) {
+  constexpr int64_t row = int64_t(1) << 20;
+  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
+}
+
 // small utility kernels (layout.hip); fills instead of hipMemsetAsync so the
 // sequence stays correct under hipGraph replay
 void fill_f32(float* p, float v, int64_t n, hipStream_t stream);

@@ -135,9 +135,7 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __r
 hipError_t launch_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, const float* dw,
                                   int64_t T, int E, int k, float* dlogits, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  // in rows of workgroups, since one row holds fewer than 2^32 threads
-  const int64_t n = (T + 3) / 4, row = 1 << 20;
-  const dim3 blocks = n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
+  const dim3 blocks = grid_rows((T + 3) / 4);
   // 16-byte stores where every row starts on a 16-byte boundary
   if (E % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0)
     router_topk_bwd_kernel<true><<<blocks, 256, 0, stream>>>(topk_ids, topk_w, dw, T, E, k, dlogits);

@@ -465,3 +465,16 @@ def test_product_of_nearly_two_to_the_31_rows(grouped):
     for got, s in zip(c[:M].view(-1).split(1 << 26), asf.view(-1).split(1 << 26)):
         assert torch.equal(got, (16 * s).to(torch.bfloat16))
     assert torch.all(c[M:] == 0)
+
+
+def test_quantize_more_weight_blocks_than_a_row_of_workgroups():
+    """2^24 + 5 weights of one block each: more threads than 2^32.  Column 0 is
+    448 times a power of two, which is the scale."""
+    G = (1 << 24) + 5
+    s = torch.exp2((torch.arange(G, device=DEV) % 9 - 4).float())
+    w = torch.zeros((G, 1, 16), dtype=torch.bfloat16, device=DEV)
+    w[:, 0, 0], w[:, 0, 15] = 448 * s, -2 * s
+    q, sf = nv.fp8_quantize_weight(w)
+    assert torch.equal(sf.view(-1), s)
+    q = q.view(torch.uint8).view(G, 16)
+    assert torch.all(q[:, 0] == 0x7E) and torch.all(q[:, 15] == 0xC0) and not q[:, 1:15].any()
