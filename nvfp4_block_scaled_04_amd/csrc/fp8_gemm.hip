@@ -55,6 +55,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
+__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Wave-uniform read through the constant address space (a scalar load); only
 // for arrays the kernel does not write.
 __device__ __forceinline__ float uniform_load(const float* p, int i) {
@@ -188,7 +190,8 @@ template <int RF, int JT, int D>
 __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) {
   constexpr int kRows = 16 * RF, kStride = kRows + 4;
   __shared__ float red[kSkWaves][16][kStride];
-  const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
+  const uint32_t wg = workgroup();
+  const int mt = wg / p.n_groups, ng = wg - mt * p.n_groups;
   RowTile t;
   if (!row_tile(p, 16 * JT, mt, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -386,7 +389,8 @@ __device__ __forceinline__ void st_stage(float4v (&acc)[2][JT], const StLoads& s
 template <int JT, int POL>
 __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params p) {
   __shared__ __align__(1024) uint8_t smem[kStWaves * kStRing * kStStage];
-  const int mt = blockIdx.x / p.n_groups, ng = blockIdx.x - mt * p.n_groups;
+  const uint32_t wg = workgroup();
+  const int mt = wg / p.n_groups, ng = wg - mt * p.n_groups;
   RowTile t;
   if (!row_tile(p, 16 * JT, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
@@ -775,8 +779,9 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   // and an expert's m tiles its weights, in one L2.
   TileList list;
   const int64_t all = (int64_t)list.count(p, p.bm) * p.n_groups, chunk = (all + 7) >> 3;
-  const int64_t at = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= chunk || at >= all) return;
+  const uint32_t wg = workgroup();             // rows of workgroups are whole rounds of the XCDs
+  const int64_t at = (int64_t)(wg & 7) * chunk + (wg >> 3);
+  if ((wg >> 3) >= chunk || at >= all) return;
   const int mt = (int)(at / p.n_groups), ng = (int)(at - (int64_t)mt * p.n_groups);
   RowTile t;
   if (!list.find(p, p.bm, mt, t)) return;
@@ -835,7 +840,7 @@ hipError_t launch_stream(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) 
   p.n_groups = (int)((a.N + kStN - 1) / kStN);
   const int64_t grid = tile_bound(a, 16 * JT) * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  fp8_stream_kernel<JT, POL><<<(unsigned)grid, kStWaves * 64, 0, stream>>>(p);
+  fp8_stream_kernel<JT, POL><<<grid_rows(grid), kStWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -844,7 +849,7 @@ hipError_t launch_skinny(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) 
   p.n_groups = (int)((a.N + 16 * RF - 1) / (16 * RF));
   const int64_t grid = tile_bound(a, 16 * JT) * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  fp8_skinny_kernel<RF, JT, D><<<(unsigned)grid, kSkWaves * 64, 0, stream>>>(p);
+  fp8_skinny_kernel<RF, JT, D><<<grid_rows(grid), kSkWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -866,7 +871,7 @@ hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
     if (err != hipSuccess) return err;
     attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  fp8_tile_kernel<POL><<<(unsigned)grid, kTlWaves * 64, kTlLds, stream>>>(p);
+  fp8_tile_kernel<POL><<<grid_rows(grid), kTlWaves * 64, kTlLds, stream>>>(p);
   return hipGetLastError();
 }
 

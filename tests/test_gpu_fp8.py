@@ -478,3 +478,21 @@ def test_quantize_more_weight_blocks_than_a_row_of_workgroups():
     assert torch.equal(sf.view(-1), s)
     q = q.view(torch.uint8).view(G, 16)
     assert torch.all(q[:, 0] == 0x7E) and torch.all(q[:, 15] == 0xC0) and not q[:, 1:15].any()
+
+
+@pytest.mark.parametrize("rows", [1, 13])
+def test_product_of_more_tiles_than_a_row_of_workgroups(rows):
+    """17 experts of 2^27 - 128 columns with 1 and 13 rows each: more than 2^32
+    threads of the streaming and of the tile kernel (42 and 96 GB)."""
+    E, N, K = 17, (1 << 27) - 128, 16
+    M = E * rows
+    print(f"[case] fp8 wide experts rows={rows} N={N}", flush=True)
+    a, asf = _ones(M, K), torch.ones((M, 1), device=DEV)
+    b = _ones(E * N, K).view(E, N, K)
+    bsf = (torch.arange(E * (N // 128), device=DEV) % 7 + 1).float().view(E, N // 128, 1)
+    off = torch.arange(0, M + 1, rows, dtype=torch.int32, device=DEV)
+    c = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+    nv.fp8_grouped_gemm(a, asf, b, bsf, offsets=off, out=c)
+    for d in range(M):
+        want = (16 * bsf[d // rows]).to(torch.bfloat16)
+        assert torch.equal(c[d].view(-1, 128), want.expand(-1, 128)), d
