@@ -443,8 +443,12 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   asm volatile("" ::: "memory");
   st_load_w<POL>(st, 2, s2);
   asm volatile("" ::: "memory");
-  // four stages a pass, those behind the last on zeros
-  auto sb = [&](int b) { return uniform_load(bsf, b < p.KB ? b : 0); };
+  // four stages a pass, those behind the last on zeros with scale 0: block 0's,
+  // which is loaded in their place, may be infinite, and 0 times that no number
+  auto sb = [&](int b) {
+    const float v = uniform_load(bsf, b < p.KB ? b : 0);
+    return b < p.KB ? v : 0.0f;
+  };
   for (int b = 0; b < p.KB; b += 4) {
     const float f0 = sb(b), f1 = sb(b + 1), f2 = sb(b + 2), f3 = sb(b + 3);
     st_stage<JT, POL>(acc, st, b, f0, x0, x2, s0, s3);

@@ -496,3 +496,28 @@ def test_product_of_more_tiles_than_a_row_of_workgroups(rows):
     for d in range(M):
         want = (16 * bsf[d // rows]).to(torch.bfloat16)
         assert torch.equal(c[d].view(-1, 128), want.expand(-1, 128)), d
+
+
+@pytest.mark.parametrize("K", [128, 272, 512, 784])
+@pytest.mark.parametrize("counts", [[30, 2], [3] * 700, [250] * 200], ids=["few_rows", "streamed", "tiles"])
+@pytest.mark.parametrize("last", [False, True])
+def test_product_infinite_weight_scale(counts, K, last):
+    """One block of one expert's weight with an infinite scale: its columns are
+    infinite with the sign of that block's sum, and no other output changes."""
+    print(f"[case] fp8 infinite weight scale K={K} experts={len(counts)} last={last}", flush=True)
+    rng = np.random.default_rng(K + len(counts))
+    M, E, N = sum(counts), len(counts), 136
+    a, asf, b, bsf = _operands(rng, M, E, N, K)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    e, kb = E // 2, bsf.shape[2] - 1 if last else 0
+    offd = torch.from_numpy(off).to(DEV)
+    clean = bf16_values(host(nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf), offsets=offd)))
+    bsf[e, 0, kb] = np.inf
+    got = bf16_values(host(nv.fp8_grouped_gemm(*_dev(a, asf, b, bsf), offsets=offd)))
+    lo, hi, k0, k1 = off[e], off[e + 1], kb * 128, min(K, kb * 128 + 128)
+    x, w = F.e4m3_decode(a[lo:hi, k0:k1]), F.e4m3_decode(b[e, :128, k0:k1])
+    dot = x @ w.T
+    sure = np.abs(dot) > 2.0 ** -8 * (np.abs(x) @ np.abs(w).T)      # far from what the sum may be off by
+    assert sure.any() and np.array_equal(got[lo:hi, :128][sure], np.sign(dot[sure]) * np.inf)
+    got[lo:hi, :128] = clean[lo:hi, :128]
+    assert np.array_equal(got, clean)
