@@ -474,6 +474,10 @@ nvfp4_status nvfp4_moe_combine_bwd(const void* dout_bf16, const void* y_bf16,
  * code * scale.  With b = max(amax of the block, 2^-100), every step in fp32,
  * round to nearest even:
  *   scale = b / 448,  r = 448 / b,  code = E4M3(v * r).
+ * A NaN does not count in amax: its own code is NaN (0x7F or 0xFF) and the
+ * block's other values keep theirs.  An infinity does: its block's scale is
+ * infinite, its own code NaN and the others' 0 (of their sign), so that all stand
+ * for NaN.
  *
  * nvfp4_fp8_quantize: v = x[row][col], row r at x + r*ld_x elements.
  * nvfp4_fp8_swiglu_quantize: x rows hold [gate | up], cols columns each;

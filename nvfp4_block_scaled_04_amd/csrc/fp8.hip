@@ -6,7 +6,9 @@
 //   scale = b / 448,  r = 448 / b,  code = E4M3(x * r).
 // |x * r| <= 448 * (1 + 2^-23), which rounds to at most 448, so no clamp is
 // needed; the 2^-100 floor keeps r finite and gives an all-zero block codes 0
-// and a positive scale.  v_cvt_pk_fp8_f32 rounds to nearest, ties to even.
+// and a positive scale.  v_cvt_pk_fp8_f32 rounds to nearest, ties to even.  fmaxf
+// passes over a NaN, so one bad value keeps its NaN code to itself; an infinity
+// gives an infinite scale and r = 0.
 //
 // All three are bound by HBM: rows read 2 and write 1 + 4/128 bytes per
 // element, SwiGLU reads 4, weights read 2 and write 1.  Sixteen lanes hold

@@ -2,7 +2,8 @@
 
 Formulas (b runs over blocks of 128 columns; the last may be shorter):
   quantise     m = max(amax of the block, 2^-100); scale = m / 448, r = 448 / m,
-               code = E4M3(x * r); fp32 operations, round to nearest even
+               code = E4M3(x * r); fp32 operations, round to nearest even; a NaN
+               does not count in amax
   SwiGLU       h = gate / (1 + exp(-gate)) * up
   product      c[d][n] = sum_b sa[s][b] sw[n/128][b] sum_{k in b} a[s][k] w[n][k]
   dispatch     rows[inv[t*k+j]] = x[t] for inv < n, else 0
@@ -22,16 +23,18 @@ _TABLE = F.e4m3_decode(np.arange(0x7F))          # 0 .. 448, ascending
 
 def e4m3_encode(v):
     """E4M3 byte nearest to each v (|v| <= 464: more would round past 448),
-    ties to the even code, sign bit taken from v."""
+    ties to the even code, sign bit taken from v; 0x7F or 0xFF for a NaN."""
     v = np.asarray(v)
-    mag = np.minimum(np.abs(v.astype(np.float64)), 448.0)
-    return F._nearest_ties_even(_TABLE, mag).astype(np.uint8) | (np.signbit(v).astype(np.uint8) << 7)
+    nan = np.isnan(v)
+    mag = np.where(nan, 0.0, np.minimum(np.abs(v.astype(np.float64)), 448.0))
+    code = np.where(nan, 0x7F, F._nearest_ties_even(_TABLE, mag)).astype(np.uint8)
+    return code | (np.signbit(v).astype(np.uint8) << 7)
 
 
 def _amax_blocks(x, br):
     R, C = x.shape
     p = np.zeros((-(-R // br) * br, -(-C // BLOCK) * BLOCK), np.float32)
-    p[:R, :C] = np.abs(x)
+    p[:R, :C] = np.fmax(np.abs(x), 0)
     return p.reshape(p.shape[0] // br, br, p.shape[1] // BLOCK, BLOCK).max(axis=(1, 3))
 
 
@@ -43,7 +46,8 @@ def quantize(x, block_rows=1):
     m = np.maximum(_amax_blocks(x, block_rows), FLOOR)
     r = np.float32(448.0) / m
     rr = np.repeat(np.repeat(r, block_rows, 0)[:R], BLOCK, 1)[:, :C]
-    return e4m3_encode(x * rr), m / np.float32(448.0)
+    with np.errstate(invalid="ignore"):                  # infinity times r = 0
+        return e4m3_encode(x * rr), m / np.float32(448.0)
 
 
 def decode(q, sf, block_rows=1):

@@ -521,3 +521,61 @@ def test_product_infinite_weight_scale(counts, K, last):
     assert sure.any() and np.array_equal(got[lo:hi, :128][sure], np.sign(dot[sure]) * np.inf)
     got[lo:hi, :128] = clean[lo:hi, :128]
     assert np.array_equal(got, clean)
+
+
+def _odd_values(rng, R, C):
+    """Activations with NaN (quiet and signalling, both signs) in every third
+    row, infinities in every fifth, and one block of nothing but NaN."""
+    x = _acts(rng, R, C)
+    for i, bits in enumerate([0x7FC0, 0xFFC0, 0x7F81, 0xFF81]):
+        x.view(torch.int16)[::3, 5 + 7 * i] = bits - (0x10000 if bits & 0x8000 else 0)
+    x[1::5, C - 3], x[2::5, 2] = float("inf"), float("-inf")
+    x[0, :128] = float("nan")
+    return x
+
+
+def _same_codes(got, want):
+    nan = want & 0x7F == 0x7F                            # of either sign
+    return np.array_equal(got & 0x7F == 0x7F, nan) and np.array_equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("R,C", [(17, 272), (600, 16384)])
+def test_quantize_nan_and_infinity(R, C):
+    """Bit-exact, but for a NaN code's sign: one and four rows a lane group."""
+    print(f"[case] fp8 odd values R={R} C={C}", flush=True)
+    x = _odd_values(np.random.default_rng(R), R, C)
+    q, sf = nv.fp8_quantize(x.to(DEV))
+    rq, rs = P.quantize(_f32(x))
+    assert np.array_equal(host(sf), rs) and _same_codes(_codes(q), rq)
+    assert np.isinf(rs).any() and (rq & 0x7F == 0x7F).any()
+
+
+@pytest.mark.parametrize("N,K", [(130, 272), (300, 160)])
+def test_quantize_weight_nan_and_infinity(N, K):
+    x = _odd_values(np.random.default_rng(N), N, K)
+    x[:128, :128].nan_to_num_(nan=float("nan"), posinf=3.0, neginf=-3.0)   # NaN alone in the first block
+    q, sf = nv.fp8_quantize_weight(x[None].to(DEV))
+    rq, rs = P.quantize(_f32(x), 128)
+    assert np.array_equal(host(sf)[0], rs) and _same_codes(_codes(q)[0], rq)
+    assert np.isfinite(rs[0, 0]) and np.isinf(rs).any()
+
+
+def test_swiglu_quantize_nan_and_infinity():
+    """A NaN gate or up value has the NaN code and leaves its block's others; an
+    infinite product takes its block."""
+    x = _acts(np.random.default_rng(5), 6, 2 * 256)
+    y = x.clone()
+    y[0, 3], y[1, 256 + 200] = float("nan"), float("nan")
+    y[2, 140], y[2, 256 + 140] = 3e38, 3e38
+    small = [(0, 3), (1, 200)]
+    for r, c in small:
+        x[r, c] = 0                                      # what the others' scale is made from
+    ref, rs = nv.fp8_swiglu_quantize(x.to(DEV))
+    q, sf = nv.fp8_swiglu_quantize(y.to(DEV))
+    got, want, s, ws = _codes(q), _codes(ref).copy(), host(sf), host(rs).copy()
+    for r, c in small:
+        assert got[r, c] & 0x7F == 0x7F
+        want[r, c] = got[r, c]
+    assert got[2, 140] & 0x7F == 0x7F and np.isinf(s[2, 1]) and not (np.delete(got[2, 128:], 12) & 0x7F).any()
+    want[2, 128:], ws[2, 1] = got[2, 128:], np.inf
+    assert np.array_equal(got, want) and np.array_equal(s, ws)

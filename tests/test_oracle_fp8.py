@@ -128,3 +128,16 @@ def test_swiglu_closed_forms():
     x = np.array([[0.0, 100.0, -100.0, 2.0, 3.0, 5.0]])
     h = P.swiglu(x)
     assert h[0, 0] == 0 and abs(h[0, 1] - 300) < 1e-9 and abs(h[0, 2]) < 1e-30
+
+
+def test_nan_keeps_to_itself_and_infinity_takes_its_block():
+    x = np.zeros((2, 256), np.float32)
+    x[0, :3] = [np.nan, 448.0, -1.0]
+    x[0, 128:131] = [-np.nan, np.nan, 0.0]               # no finite magnitude: the floor
+    x[1, :3] = [-np.inf, 5.0, np.nan]
+    x[1, 128] = 224.0
+    q, sf = P.quantize(x)
+    assert list(q[0, :3]) == [0x7F, 0x7E, 0xB8] and sf[0, 0] == 1.0
+    assert q[0, 128] & 0x7F == 0x7F and q[0, 129] == 0x7F and sf[0, 1] == np.float32(2.0 ** -100) / np.float32(448)
+    assert q[1, 0] & 0x7F == 0x7F and q[1, 1] == 0 and q[1, 2] == 0x7F and sf[1, 0] == np.inf
+    assert q[1, 128] == 0x7E and sf[1, 1] == 0.5
