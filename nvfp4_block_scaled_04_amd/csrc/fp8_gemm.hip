@@ -967,6 +967,17 @@ extern "C" int nvfp4_internal_fp8_cut(int64_t M, int lo, int hi, int bm, int i, 
   return TileList::tiles(lo, hi, bm);
 }
 
+// The choice of kernel on `cus` CUs, for the tests that each kernel is run by
+// sizes meant for it: plan = {kind, RF, JT, tile height}.
+extern "C" void nvfp4_internal_fp8_plan(int E, int grouped, int64_t M, int64_t N, int64_t K, int cus, int* plan) {
+  static const int32_t some = 0;
+  Fp8GemmArgs a{};
+  a.offsets = grouped ? &some : nullptr;
+  a.E = E; a.M = M; a.N = N; a.K = K;
+  const Fp8Plan p = plan_of(a, cus);
+  plan[0] = p.kind; plan[1] = p.rf; plan[2] = p.jt; plan[3] = p.bm;
+}
+
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   Fp8Params p;
   p.a_q = a.a_q; p.a_sf = a.a_sf; p.rows_a = a.rows_a; p.a_row_src = a.a_row_src;
