@@ -514,7 +514,11 @@ nvfp4_status nvfp4_fp8_quantize_weight(const void* w_bf16, int64_t groups, int64
  * b_q uint8 [E][N][K], b_sf float [E][ceil(N/128)][ceil(K/128)]
  * (nvfp4_fp8_quantize_weight; row-major, no packing); c BF16 [M][N].
  * The gradient with respect to A is the same product of the quantised output
- * gradient with the transposed weights (nvfp4_weight_layout transposes).
+ * gradient with the transposed weights: codes [E][K][N] and scales
+ * [E][ceil(K/128)][ceil(N/128)], the elements of both as they are (a 128 x 128
+ * block keeps its scale); N % 16 == 0.  The caller transposes them, once
+ * (nvfp4_weight_layout takes BF16 weights only).  The gradients of the weights
+ * and of SwiGLU are not part of this library.
  * Shapes: M >= 0, 1 <= E <= 4096, N >= 1, 16 <= K < 2^22, K % 16 == 0,
  *   N*K < 2^31; with a_row_src also rows_a*K < 2^31 and a_row_div >= 1,
  *   without it rows_a >= M.  a_q, b_q 16-byte aligned.  No workspace.

@@ -295,3 +295,73 @@ def test_gradients_replay_from_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), r
+
+
+def test_gradients_chained_from_the_output_to_the_tokens():
+    """The backward pass of dispatch, product, SwiGLU, product, combine, each
+    link fed the gradient that the one before gave: combine, the product with the
+    transposed second weight, SwiGLU (its gradient here in PyTorch), the product
+    with the transposed first weight, dispatch.  The transposed weights are the
+    forward's own codes and 128 x 128 scales, both transposed.  Each link
+    against float64 on its device inputs, with that link's bound, in the host's
+    own order of rows and slots; pairs without an expert among them."""
+    rng = np.random.default_rng(77)
+    T, H, I, E, k = 45, 272, 144, 5, 3
+    x = _bf(rng, T, H).to(DEV)
+    ids, off, perm, inv = _routing(rng, T, k, E, 0.15)
+    n, hinv, hoff = int(off[-1]), host(inv), host(off)
+    assert n < T * k
+    w = torch.from_numpy(rng.random((T, k)).astype(np.float32)).to(DEV)
+    b1, s1 = nv.fp8_quantize_weight((_bf(rng, E, 2 * I, H) * 0.1).to(DEV))
+    b2, s2 = nv.fp8_quantize_weight((_bf(rng, E, H, I) * 0.1).to(DEV))
+
+    def transposed(b, s):
+        return b.view(torch.uint8).transpose(1, 2).contiguous().view(b.dtype), s.transpose(1, 2).contiguous()
+
+    q, sf = nv.fp8_quantize(x)
+    y1 = nv.fp8_grouped_gemm(q, sf, b1, s1, offsets=off, M=T * k, a_row_src=perm, a_row_div=k)
+    h, hs = nv.fp8_swiglu_quantize(y1, offsets=off)
+    y = nv.fp8_grouped_gemm(h, hs, b2, s2, offsets=off)
+    dout = _bf(rng, T, H).to(DEV)
+    dy, dw = nv.moe_combine_bwd(dout, y, inv, w, off)
+    qy = nv.fp8_quantize(dy)
+    dh = nv.fp8_grouped_gemm(*qy, *transposed(b2, s2), offsets=off)
+    gate, up, d = y1[:n, :I].float(), y1[:n, I:].float(), dh[:n].float()
+    sig = torch.sigmoid(gate)
+    dy1 = torch.zeros((T * k, 2 * I), dtype=torch.bfloat16, device=DEV)
+    dy1[:n, :I] = d * up * sig * (1 + gate * (1 - sig))
+    dy1[:n, I:] = d * gate * sig
+    q1 = nv.fp8_quantize(dy1)
+    drows = nv.fp8_grouped_gemm(*q1, *transposed(b1, s1), offsets=off)
+    dx = nv.moe_dispatch_bwd(drows, inv, off, k)
+    torch.cuda.synchronize()
+
+    f64 = lambda t: bf16_values(host(t))
+    codes = lambda t: t.view(torch.uint8).cpu().numpy()
+    # combine: row inv[t*k+j] is w[t][j] dout[t], rounded once
+    rdy = np.zeros((T * k, H))
+    for f in range(T * k):
+        if hinv[f] < n:
+            assert ids[f // k, f % k] == np.searchsorted(hoff, hinv[f], side="right") - 1
+            rdy[hinv[f]] = float(w[f // k, f % k]) * f64(dout)[f // k]
+    assert np.all(np.abs(f64(dy) - rdy) <= 2.0 ** -8 * np.abs(rdy) * (1 + 2.0 ** -16))
+    # both products against the weights as they were quantised for the forward, transposed in float64
+    for got, (qa, sa), (b, s) in ((dh, qy, (b2, s2)), (drows, q1, (b1, s1))):
+        wl = [P.decode(codes(b)[e], host(s)[e], 128).T for e in range(E)]
+        ref, mag, peak = P.grouped_product(P.decode(codes(qa), host(sa)), wl, hoff, np.arange(T * k))
+        kb = -(-qa.shape[1] // 128)
+        bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * ((128 + 2 + kb + 8) * 2.0 ** -23 * mag + 7 * 2.0 ** -13 * peak)
+        assert np.all((np.abs(f64(got) - ref) <= bound)[:n])
+    # dispatch: each token's rows, in its slots' order
+    ref, mag = P.dispatch_bwd(f64(drows), hinv, n, k)
+    assert np.all(np.abs(f64(dx) - ref) <= 2.0 ** -8 * np.abs(ref) + k * 2.0 ** -24 * mag)
+    none = (hinv.reshape(T, k) >= n).all(1)
+    assert np.all(f64(dx)[none] == 0) and np.any(f64(dx)[~none] != 0)
+    # SwiGLU's formula above against differences, in float64
+    g, u, dd = (t.double().cpu().numpy() for t in (gate, up, d))
+    eps = 1e-6
+    silu = lambda v: v / (1 + np.exp(-v))
+    for col, diff in ((0, (silu(g + eps) - silu(g - eps)) / (2 * eps) * u * dd), (I, silu(g) * dd)):
+        have = f64(dy1)[:n, col:col + I]
+        # one BF16 rounding, eight fp32 operations on terms up to (1 + |g|) the factors, the quotient's own 1e-9
+        assert np.all(np.abs(have - diff) <= 2.0 ** -8 * np.abs(diff) + (16 * 2.0 ** -23 + 1e-9) * (1 + np.abs(g)) ** 2 * (1 + np.abs(u)) * np.abs(dd))
