@@ -46,7 +46,7 @@ template <int TPT>
 __device__ __forceinline__ int64_t my_token(int& tid) {
   constexpr int per = TPT >= kGroupThreads ? 1 : kGroupThreads / TPT;
   tid = threadIdx.x % TPT;
-  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * per + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
+  return (int64_t)row_workgroup() * per + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
 }
 
 // Reads of a token's slots through the constant address space: scalar loads,

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
     const int64_t n = n_rows[0];
     rows = n < rows ? n : rows;
   }
-  const uint32_t unit = (blockIdx.y * gridDim.x + blockIdx.x) * kQGroups + (threadIdx.x >> 4);
+  const uint32_t unit = row_workgroup() * kQGroups + (threadIdx.x >> 4);
   const uint32_t chunk = unit / (uint32_t)kblocks;
   const int kb = (int)(unit - chunk * (uint32_t)kblocks);
   const int64_t row0 = (int64_t)chunk * ROWS;
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
 __global__ __launch_bounds__(kQThreads) void fp8_weight_kernel(
     const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks, uint32_t units,
     uint8_t* __restrict__ q, float* __restrict__ sf) {
-  const uint32_t unit = blockIdx.y * gridDim.x + blockIdx.x;
+  const uint32_t unit = row_workgroup();
   if (unit >= units) return;
   const uint32_t t = unit / (uint32_t)kblocks;
   const int kb = (int)(unit - t * (uint32_t)kblocks);

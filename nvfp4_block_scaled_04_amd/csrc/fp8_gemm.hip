@@ -55,8 +55,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
-__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y * gridDim.x + blockIdx.x; }
-
 // Wave-uniform read through the constant address space (a scalar load); only
 // for arrays the kernel does not write.
 __device__ __forceinline__ float uniform_load(const float* p, int i) {
@@ -190,7 +188,7 @@ template <int RF, int JT, int D>
 __global__ __launch_bounds__(kSkWaves * 64) void fp8_skinny_kernel(Fp8Params p) {
   constexpr int kRows = 16 * RF, kStride = kRows + 4;
   __shared__ float red[kSkWaves][16][kStride];
-  const uint32_t wg = workgroup();
+  const uint32_t wg = row_workgroup();
   const int mt = wg / p.n_groups, ng = wg - mt * p.n_groups;
   RowTile t;
   if (!row_tile(p, 16 * JT, mt, t)) return;
@@ -389,7 +387,7 @@ __device__ __forceinline__ void st_stage(float4v (&acc)[2][JT], const StLoads& s
 template <int JT, int POL>
 __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params p) {
   __shared__ __align__(1024) uint8_t smem[kStWaves * kStRing * kStStage];
-  const uint32_t wg = workgroup();
+  const uint32_t wg = row_workgroup();
   const int mt = wg / p.n_groups, ng = wg - mt * p.n_groups;
   RowTile t;
   if (!row_tile(p, 16 * JT, mt, t)) return;
@@ -783,7 +781,7 @@ __global__ __launch_bounds__(kTlWaves * 64, 2) void fp8_tile_kernel(Fp8Params p)
   // and an expert's m tiles its weights, in one L2.
   TileList list;
   const int64_t all = (int64_t)list.count(p, p.bm) * p.n_groups, chunk = (all + 7) >> 3;
-  const uint32_t wg = workgroup();             // rows of workgroups are whole rounds of the XCDs
+  const uint32_t wg = row_workgroup();             // rows of workgroups are whole rounds of the XCDs
   const int64_t at = (int64_t)(wg & 7) * chunk + (wg >> 3);
   if ((wg >> 3) >= chunk || at >= all) return;
   const int mt = (int)(at / p.n_groups), ng = (int)(at - (int64_t)mt * p.n_groups);

@@ -12,11 +12,14 @@ namespace nvfp4 {
 
 // Grid of n (< 2^31) workgroups of up to 1024 threads in rows of 2^20: one row
 // of 2^32 threads or more would wrap without an error.  A kernel's workgroup is
-// blockIdx.y * gridDim.x + blockIdx.x, and those behind the n-th have no work.
+// row_workgroup(), and those behind the n-th have no work.
+constexpr int kGridRowShift = 20;
 inline dim3 grid_rows(int64_t n) {
-  constexpr int64_t row = int64_t(1) << 20;
+  constexpr int64_t row = int64_t(1) << kGridRowShift;
   return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
 }
+// without a read of gridDim, which comes from memory
+__device__ __forceinline__ uint32_t row_workgroup() { return (blockIdx.y << kGridRowShift) + blockIdx.x; }
 
 // small utility kernels (layout.hip); fills instead of hipMemsetAsync so the
 // sequence stays correct under hipGraph replay

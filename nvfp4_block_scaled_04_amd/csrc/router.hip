@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const int32_t* __r
                                                               float* __restrict__ dlogits) {
 #pragma clang fp contract(off)   // else w * g would round differently lane by lane in the exchanges
   const int lane = threadIdx.x & 63;
-  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t t = (int64_t)row_workgroup() * 4 + (threadIdx.x >> 6);
   if (t >= T) return;                          // the whole wave
   float w = 0.0f, g = 0.0f;
   int id = -1;
