@@ -90,8 +90,15 @@ hipError_t launch_combine(const void* y, const int32_t* inv_perm, const float* t
                           const int32_t* offsets, int64_t T, int k, int E, int64_t H, void* out,
                           hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  combine_kernel<<<(unsigned)T, kThreads, 0, stream>>>(
-      static_cast<const uint4*>(y), inv_perm, topk_w, offsets, k, E, H, static_cast<uint4*>(out));
+  // In pieces of 2^22 tokens, since a launch of 2^32 threads or more would wrap
+  // without an error.  (A bound check in the kernel, for a grid in two
+  // dimensions, takes 10% of a small call: 1000 x 6 x 512, 4.3 -> 4.8 us.)
+  constexpr int64_t kPiece = int64_t(1) << 22;
+  for (int64_t t = 0; t < T; t += kPiece) {
+    combine_kernel<<<(unsigned)(T - t < kPiece ? T - t : kPiece), kThreads, 0, stream>>>(
+        static_cast<const uint4*>(y), inv_perm + t * k, topk_w + t * k, offsets, k, E, H,
+        static_cast<uint4*>(out) + t * (H / 8));
+  }
   return hipGetLastError();
 }
 

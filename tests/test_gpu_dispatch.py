@@ -365,3 +365,16 @@ def test_gradients_chained_from_the_output_to_the_tokens():
         have = f64(dy1)[:n, col:col + I]
         # one BF16 rounding, eight fp32 operations on terms up to (1 + |g|) the factors, the quotient's own 1e-9
         assert np.all(np.abs(have - diff) <= 2.0 ** -8 * np.abs(diff) + (16 * 2.0 ** -23 + 1e-9) * (1 + np.abs(g)) ** 2 * (1 + np.abs(u)) * np.abs(dd))
+
+
+def test_combine_of_more_tokens_than_a_row_of_workgroups():
+    """6 million tokens of eight columns, 896 threads each: more than 2^32."""
+    T = 6_000_011
+    g = torch.Generator(DEV).manual_seed(2)
+    inv = torch.randperm(T, device=DEV, generator=g)
+    y = torch.randn((T, 8), device=DEV, generator=g).to(torch.bfloat16)
+    off = torch.tensor([0, T - 3], dtype=torch.int32, device=DEV)
+    out = torch.full((T, 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    nv.moe_combine(y, inv.to(torch.int32), torch.full((T, 1), 0.5, device=DEV), off, out=out)
+    want = torch.where((inv < T - 3)[:, None], y[inv] * 0.5, torch.zeros_like(y))
+    assert torch.equal(out, want)
