@@ -147,8 +147,13 @@ hipError_t launch_router_topk_bwd(const int32_t* topk_ids, const float* topk_w, 
 hipError_t launch_router_topk(const float* logits, int64_t T, int E, int k, int32_t* topk_ids,
                               float* topk_w, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const int64_t blocks = (T + 3) / 4;
-  router_topk_kernel<<<(unsigned)blocks, 256, 0, stream>>>(logits, T, E, k, topk_ids, topk_w);
+  // in pieces, since a launch of 2^32 threads or more would wrap without an error
+  constexpr int64_t kPiece = int64_t(1) << 24;
+  for (int64_t t = 0; t < T; t += kPiece) {
+    const int64_t n = T - t < kPiece ? T - t : kPiece;
+    router_topk_kernel<<<(unsigned)((n + 3) / 4), 256, 0, stream>>>(logits + t * E, n, E, k, topk_ids + t * k,
+                                                                    topk_w + t * k);
+  }
   return hipGetLastError();
 }
 

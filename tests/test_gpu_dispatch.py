@@ -378,3 +378,11 @@ def test_combine_of_more_tokens_than_a_row_of_workgroups():
     nv.moe_combine(y, inv.to(torch.int32), torch.full((T, 1), 0.5, device=DEV), off, out=out)
     want = torch.where((inv < T - 3)[:, None], y[inv] * 0.5, torch.zeros_like(y))
     assert torch.equal(out, want)
+
+
+def test_router_of_more_tokens_than_a_row_of_workgroups():
+    """2^26 + 5 tokens, a wave each: more than 2^32 threads."""
+    T = (1 << 26) + 5
+    lg = torch.randn((T, 2), device=DEV, generator=torch.Generator(DEV).manual_seed(4))
+    ids, w = nv.router_topk(lg, 1)
+    assert torch.equal(ids[:, 0], (lg[:, 1] > lg[:, 0]).to(torch.int32)) and torch.all(w == 1)
