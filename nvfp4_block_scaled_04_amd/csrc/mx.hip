@@ -76,9 +76,14 @@ hipError_t launch_mx_reencode(const uint8_t* q, const uint8_t* sf, int64_t rows,
                               uint8_t* q_mx, uint8_t* sc_mx, hipStream_t stream) {
   const int64_t nblocks = rows * (cols / 32);
   if (nblocks == 0) return hipSuccess;
-  mx_reencode_kernel<<<(unsigned)((nblocks + 255) / 256), 256, 0, stream>>>(
-      reinterpret_cast<const uint4*>(q), reinterpret_cast<const uint16_t*>(sf), nblocks,
-      reinterpret_cast<uint4*>(q_mx), reinterpret_cast<uint16_t*>(sc_mx));
+  // in pieces, since a launch of 2^32 threads or more would wrap without an error
+  constexpr int64_t kPiece = int64_t(1) << 30;
+  for (int64_t b = 0; b < nblocks; b += kPiece) {
+    const int64_t n = nblocks - b < kPiece ? nblocks - b : kPiece;
+    mx_reencode_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+        reinterpret_cast<const uint4*>(q) + b, reinterpret_cast<const uint16_t*>(sf) + b, n,
+        reinterpret_cast<uint4*>(q_mx) + b, reinterpret_cast<uint16_t*>(sc_mx) + b);
+  }
   return hipGetLastError();
 }
 

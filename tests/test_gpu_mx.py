@@ -187,3 +187,20 @@ def test_mx_dense_config2_sampled_rows(split):
     bmq, bmsc = X.nvfp4_to_mx(bq, bsf)
     ref = X.mx_matmul(amq, amsc, gsa, bmq, bmsc, gsb[0])
     assert_close(bf16_values(host(c))[rows], bf16_values(O.round_to_bf16(ref)), "mx dense (sampled rows)", bf16=True)
+
+
+def test_to_mx_of_more_blocks_than_two_to_the_32():
+    """2^32 + 2^22 blocks of 32 in place (77 GB), one piece of 2^22 repeated:
+    every repetition equals the piece re-encoded by itself."""
+    n, rows, cols = 1025, 1 << 13, 1 << 14
+    q, sf = _random_nvfp4_bytes(64, cols, 9)
+    pq, ps = (torch.from_numpy(v).to(DEV).repeat(rows // 64, 1) for v in (q, sf))
+    gq = torch.empty((n * rows, cols // 2), dtype=torch.uint8, device=DEV)
+    gs = torch.empty((n * rows, cols // 16), dtype=torch.uint8, device=DEV)
+    for a, b in zip(gq.split(rows), gs.split(rows)):
+        a.copy_(pq)
+        b.copy_(ps)
+    nv.to_mx(gq, gs, out=(gq, gs))
+    wq, ws = nv.to_mx(pq, ps)
+    for i, (a, b) in enumerate(zip(gq.split(rows), gs.split(rows))):
+        assert torch.equal(a, wq) and torch.equal(b, ws), i
