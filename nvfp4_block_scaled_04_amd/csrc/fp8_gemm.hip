@@ -306,28 +306,27 @@ __device__ __forceinline__ lds_ptr_t lds_addr(const uint8_t* p) {
 
 // ------------------------------------------------------------ few rows, many experts
 //
-// 128 weight rows x up to 16*JT tokens per workgroup of four waves.  A wave
+// 128 weight rows x up to 16 tokens per workgroup of four waves.  A wave
 // streams its own 32 weight rows through a ring of four LDS stages (4 KB of one
 // K block each), three stages ahead and past the caches (each weight is read
 // once), so no wave waits for another.  The tokens, the same for all waves and
 // n tiles, come from L1/L2 straight to registers two stages ahead.
 // HBM-bound: what the ring keeps in flight (96 KB a CU at two workgroups) is
 // what counts.  Measured: 2048 rows over 256 experts, N 4096, K 7168 in
-// 1.11 ms, 6.8 TB/s of weights (such a read alone reaches 7.1).  Chunk q of a row lies at place q ^ ((row >> 1) & 7): no bank
-// conflicts in the fragment reads.
+// 1.11 ms, 6.8 TB/s of weights (such a read alone reaches 7.1).  Chunk q of a row
+// lies at place q ^ ((row >> 1) & 7): no bank conflicts in the fragment reads.
 
 constexpr int kStWaves = 4, kStN = 128, kStRing = 4;
 constexpr int kStStage = 32 * 128;                    // LDS bytes of a wave's stage
 
-template <int JT>
 struct StTok {
-  int8v t[JT];
-  float s[JT];
+  int8v t;
+  float s;
 };
 
 struct StLoads {
   __amdgpu_buffer_rsrc_t ra, rs, rb;
-  uint32_t wo[4], to[4], so[4];         // byte offsets of this lane's chunks and scales
+  uint32_t wo[4], to, so;               // byte offsets of this lane's chunks and scales
   uint32_t w_cut[2], t_cut_lo, t_cut_hi;   // kNowhere for chunks behind K in the last block (w: even, odd loads)
   int KB, at0, at1;                     // at0, at1: this lane's fragment chunks in a stage
 };
@@ -342,55 +341,47 @@ __device__ __forceinline__ void st_load_w(const StLoads& st, int b, uint8_t* dst
     __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rb, lds_addr(dst + c * 1024), 16, st.wo[c] | (c & 1 ? c1 : c0), b < st.KB ? b * 128 : 0, 0, POL);
 }
 
-template <int JT>
-__device__ __forceinline__ void st_load_t(const StLoads& st, int b, StTok<JT>& x) {
+__device__ __forceinline__ void st_load_t(const StLoads& st, int b, StTok& x) {
   const bool none = b >= st.KB, last = b == st.KB - 1;
   const uint32_t lo = none ? kNowhere : last ? st.t_cut_lo : 0, hi = none ? kNowhere : last ? st.t_cut_hi : 0;
   const int at = none ? 0 : b * 128;
-#pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    x.t[j] = join(__builtin_amdgcn_raw_buffer_load_b128(st.ra, st.to[j] | lo, at, 0),
-                  __builtin_amdgcn_raw_buffer_load_b128(st.ra, (st.to[j] + 64) | hi, at, 0));
-    x.s[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(st.rs, st.so[j] | (none ? kNowhere : 0), none ? 0 : b * 4, 0));
-  }
+  x.t = join(__builtin_amdgcn_raw_buffer_load_b128(st.ra, st.to | lo, at, 0),
+             __builtin_amdgcn_raw_buffer_load_b128(st.ra, (st.to + 64) | hi, at, 0));
+  x.s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(st.rs, st.so | (none ? kNowhere : 0), none ? 0 : b * 4, 0));
 }
 
 // Stage b: loads of the weights of b + 3 and the tokens of b + 2, products of
 // b.  cur and nxt are __restrict__: the fragment reads get no wait on the
 // direct loads in flight beyond the one written here.
-template <int JT, int POL>
-__device__ __forceinline__ void st_stage(float4v (&acc)[2][JT], const StLoads& st, int b, float sb, const StTok<JT>& x,
-                                         StTok<JT>& ahead, const uint8_t* __restrict__ cur,
+template <int POL>
+__device__ __forceinline__ void st_stage(float4v (&acc)[2], const StLoads& st, int b, float sb, const StTok& x, StTok& ahead, const uint8_t* __restrict__ cur,
                                          uint8_t* __restrict__ nxt) {
-  st_load_t<JT>(st, b + 2, ahead);
+  st_load_t(st, b + 2, ahead);
   asm volatile("" ::: "memory");       // the count below relies on this order
   st_load_w<POL>(st, b + 3, nxt);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStRing - 1) * (4 + 3 * JT)) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStRing - 1) * (4 + 3)) : "memory");
   int8v w[2];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
     w[f] = join(*reinterpret_cast<const int4v*>(cur + f * 2048 + st.at0), *reinterpret_cast<const int4v*>(cur + f * 2048 + st.at1));
+  const float s = x.s * sb;
 #pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    const float s = x.s[j] * sb;
+  for (int f = 0; f < 2; ++f) {
+    const float4v d = mfma_block(w[f], x.t);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const float4v d = mfma_block(w[f], x.t[j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[f][j][i] = fmaf(d[i], s, acc[f][j][i]);
-    }
+    for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], s, acc[f][i]);
   }
   // the reads of cur are done before the next stage's loads reuse it
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-template <int JT, int POL>
+template <int POL>
 __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params p) {
   __shared__ __align__(1024) uint8_t smem[kStWaves * kStRing * kStStage];
   const uint32_t wg = row_workgroup();
   const int mt = wg / p.n_groups, ng = wg - mt * p.n_groups;
   RowTile t;
-  if (!row_tile(p, 16 * JT, mt, t)) return;
+  if (!row_tile(p, 16, mt, t)) return;
   t.e = __builtin_amdgcn_readfirstlane(t.e);
   t.nrows = __builtin_amdgcn_readfirstlane(t.nrows);
   t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
@@ -401,15 +392,12 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   const int64_t a_rows = p.a_row_src ? p.rows_a : t.nrows;
   const float* bsf = p.b_sf + ((int64_t)t.e * p.NB + ng) * p.KB;
   StLoads st;
-  float4v acc[2][JT];
+  float4v acc[2];
   st.ra = rsrc_of(p.a_q + a_base * K, a_rows * K);
   st.rs = rsrc_of(p.a_sf + a_base * p.KB, a_rows * p.KB * 4);
   st.rb = rsrc_of(p.b_q + (int64_t)t.e * p.N * K, p.N * K);
   st.KB = p.KB;
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) acc[f][j] = float4v{0, 0, 0, 0};
+  acc[0] = acc[1] = float4v{0, 0, 0, 0};
   const int tail = p.K - (p.KB - 1) * 128;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -417,12 +405,9 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
     st.wo[c] = nw + row < p.N ? (uint32_t)((nw + row) * K) + 16 * q : kNowhere;
     if (c < 2) st.w_cut[c] = 16 * q < tail ? 0 : kNowhere;   // rows 16 apart have one chunk order
   }
-#pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    const int64_t row = a_row(p, t, 16 * j + r);
-    st.to[j] = row >= 0 ? (uint32_t)((row - a_base) * K) + 16 * g : kNowhere;
-    st.so[j] = row >= 0 ? (uint32_t)((row - a_base) * p.KB * 4) : kNowhere;
-  }
+  const int64_t row = a_row(p, t, r);
+  st.to = row >= 0 ? (uint32_t)((row - a_base) * K) + 16 * g : kNowhere;
+  st.so = row >= 0 ? (uint32_t)((row - a_base) * p.KB * 4) : kNowhere;
   st.t_cut_lo = 16 * g < tail ? 0 : kNowhere;
   st.t_cut_hi = 64 + 16 * g < tail ? 0 : kNowhere;
   st.at0 = r * 128 + (g ^ ((r >> 1) & 7)) * 16;
@@ -430,14 +415,14 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   uint8_t* ring = smem + wave * (kStRing * kStStage);
   uint8_t *s0 = ring, *s1 = ring + kStStage, *s2 = ring + 2 * kStStage, *s3 = ring + 3 * kStStage;
 
-  StTok<JT> x0, x1, x2, x3;
+  StTok x0, x1, x2, x3;
   st_load_w<POL>(st, 0, s0);
   asm volatile("" ::: "memory");
-  st_load_t<JT>(st, 0, x0);
+  st_load_t(st, 0, x0);
   asm volatile("" ::: "memory");
   st_load_w<POL>(st, 1, s1);
   asm volatile("" ::: "memory");
-  st_load_t<JT>(st, 1, x1);
+  st_load_t(st, 1, x1);
   asm volatile("" ::: "memory");
   st_load_w<POL>(st, 2, s2);
   asm volatile("" ::: "memory");
@@ -449,31 +434,28 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
   };
   for (int b = 0; b < p.KB; b += 4) {
     const float f0 = sb(b), f1 = sb(b + 1), f2 = sb(b + 2), f3 = sb(b + 3);
-    st_stage<JT, POL>(acc, st, b, f0, x0, x2, s0, s3);
-    st_stage<JT, POL>(acc, st, b + 1, f1, x1, x3, s1, s0);
-    st_stage<JT, POL>(acc, st, b + 2, f2, x2, x0, s2, s1);
-    st_stage<JT, POL>(acc, st, b + 3, f3, x3, x1, s3, s2);
+    st_stage<POL>(acc, st, b, f0, x0, x2, s0, s3);
+    st_stage<POL>(acc, st, b + 1, f1, x1, x3, s1, s0);
+    st_stage<POL>(acc, st, b + 2, f2, x2, x0, s2, s1);
+    st_stage<POL>(acc, st, b + 3, f3, x3, x1, s3, s2);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 7) == 0;
+  if (r >= t.nrows) return;
 #pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    if (16 * j + r >= t.nrows) continue;
+  for (int f = 0; f < 2; ++f) {
+    const int64_t n = nw + 16 * f + 4 * g;
+    if (n >= p.N) continue;
+    uint16_t* dst = p.c + (t.row0 + r) * p.N + n;
+    uint2 o;
+    o.x = pack_bf16x2(acc[f][0], acc[f][1]);
+    o.y = pack_bf16x2(acc[f][2], acc[f][3]);
+    if (vec) {
+      *reinterpret_cast<uint2*>(dst) = o;
+    } else {
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int64_t n = nw + 16 * f + 4 * g;
-      if (n >= p.N) continue;
-      uint16_t* dst = p.c + (t.row0 + 16 * j + r) * p.N + n;
-      uint2 o;
-      o.x = pack_bf16x2(acc[f][j][0], acc[f][j][1]);
-      o.y = pack_bf16x2(acc[f][j][2], acc[f][j][3]);
-      if (vec) {
-        *reinterpret_cast<uint2*>(dst) = o;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < p.N) dst[i] = (uint16_t)((i < 2 ? o.x : o.y) >> (16 * (i & 1)));
-      }
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) dst[i] = (uint16_t)((i < 2 ? o.x : o.y) >> (16 * (i & 1)));
     }
   }
 }
@@ -837,12 +819,12 @@ int64_t tile_bound(const Fp8GemmArgs& a, int bm) {
   return b < a.M ? b : a.M;
 }
 
-template <int JT, int POL>
+template <int POL>
 hipError_t launch_stream(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   p.n_groups = (int)((a.N + kStN - 1) / kStN);
-  const int64_t grid = tile_bound(a, 16 * JT) * p.n_groups;
+  const int64_t grid = tile_bound(a, 16) * p.n_groups;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  fp8_stream_kernel<JT, POL><<<grid_rows(grid), kStWaves * 64, 0, stream>>>(p);
+  fp8_stream_kernel<POL><<<grid_rows(grid), kStWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -992,7 +974,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   // bytes: two K blocks then share a line, which would be fetched twice (40
   // experts of 115 rows, N 1001, K 1040: 24 us, 32 us past the caches).
   const bool aligned = a.K % 128 == 0;
-  if (plan.kind == 0) return aligned ? launch_stream<1, 2>(a, p, stream) : launch_stream<1, 0>(a, p, stream);
+  if (plan.kind == 0) return aligned ? launch_stream<2>(a, p, stream) : launch_stream<0>(a, p, stream);
   if (plan.kind == 2)   // once: where an expert is one tile on average
     return aligned && a.M <= plan.bm * (int64_t)a.E ? launch_tile<2>(a, p, stream) : launch_tile<0>(a, p, stream);
   switch (plan.rf * 8 + plan.jt) {
