@@ -19,6 +19,17 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 
+// The eight bf16 of a 16-byte vector (uint4 or four-element vector type) as fp32
+template <typename V>
+__device__ __forceinline__ void unpack8(const V& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
 // Two floats -> two bf16 (lo in the low half), round to nearest even: one
 // v_cvt_pk_bf16_f32 on gfx950.
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));

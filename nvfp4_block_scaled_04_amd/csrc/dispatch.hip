@@ -26,13 +26,6 @@ constexpr int kBatch = 8;
 __device__ __forceinline__ u32x4 load_nt(const u32x4* p) { return __builtin_nontemporal_load(p); }
 __device__ __forceinline__ void store_nt(const u32x4& v, u32x4* p) { __builtin_nontemporal_store(v, p); }
 
-__device__ __forceinline__ void unpack8(const u32x4& v, float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_to_f32(v[i] & 0xFFFFu);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-  }
-}
 __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   return u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                pack_bf16x2(x[6], x[7])};

@@ -28,15 +28,6 @@ constexpr float kFp8Floor = 7.888609052210118e-31f;   // 2^-100
 constexpr int kQThreads = 256;
 constexpr int kQGroups = kQThreads / 16;              // blocks of 128 per pass of a workgroup
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
   float m = 0.0f;
 #pragma unroll
