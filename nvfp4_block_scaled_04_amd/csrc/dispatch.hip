@@ -10,9 +10,10 @@
 // token touches every row exactly once: no atomics, a fixed summation order,
 // and each token row is read once for its k expert rows.  All are bound by
 // HBM (16-byte vectors, kBatch rows in flight per thread).  Measured with 8192
-// tokens x 8 rows of 7168: dispatch 184 us and its gradient 182 us (1.06 GB:
-// 5.8 TB/s), combine's gradient 350 to 405 us (2.0 GB: 4.9 to
-// 5.7 TB/s); a large copy reaches 4.9 TB/s.  256 tokens: dispatch 6.6 us.
+// tokens x 8 rows of 7168: dispatch 185 us in a graph's replays, 221 traced call
+// by call, its gradient 181 to 187 us (1.06 GB: 5.8, 4.8 and 5.7 TB/s),
+// combine's gradient 335 to 408 us, by the machine (2.0 GB: 4.9 to 6.0 TB/s); a
+// large copy reaches 4.9 TB/s.  256 tokens: dispatch 6.5 to 6.8 us.
 #include "internal.hpp"
 #include "device.hpp"
 

@@ -14,8 +14,9 @@
 // element, SwiGLU reads 4, weights read 2 and write 1.  Sixteen lanes hold
 // one 128-column block, 16 bytes (8 BF16) each, so its maximum is four lane
 // exchanges and nothing is read twice.  Measured: 8192 rows of 7168 29 us
-// (178 MB: 6.1 TB/s); SwiGLU of 65536 x 2048 126 us (5.4 TB/s), of
-// 2048 x 2048 6.2 us (latency); weights 32 x 4096 x 7168 517 us (2.8 GB: 5.4 TB/s).
+// (178 MB: 6.1 TB/s); SwiGLU of 65536 x 2048 122 to 126 us (5.4 TB/s), of
+// 2048 x 2048 6.2 to 6.6 us (latency); weights 32 x 4096 x 7168 520 us (2.8 GB:
+// 5.4 TB/s).
 #include "internal.hpp"
 #include "device.hpp"
 

@@ -171,8 +171,9 @@ __device__ __forceinline__ float4v mfma_block(const int8v& w, const int8v& t) {
 // eight waves split the K blocks (block b to wave b % 8, so the workgroup reads
 // 1 KiB runs of each weight row), D blocks in flight per wave, and join
 // through LDS in wave order.  Bound by latency: the fewer rows, the more
-// workgroups pull at once.  Measured at K 7168, N 2048: one token 7.2 us
-// (14.7 MB: 2.0 TB/s, of which 2.6 us are an empty launch), 512 tokens 35 us.
+// workgroups pull at once.  Measured at K 7168, N 2048: one token 7.1 to 7.4 us
+// (14.7 MB: 2.0 TB/s, of which 2.6 us are an empty launch; N 2048 makes 128
+// workgroups, half as many as CUs), 512 tokens 36 us.
 
 constexpr int kSkWaves = 8;
 
@@ -315,7 +316,7 @@ __device__ __forceinline__ lds_ptr_t lds_addr(const uint8_t* p) {
 // n tiles, come from L1/L2 straight to registers two stages ahead.
 // HBM-bound: what the ring keeps in flight (96 KB a CU at two workgroups) is
 // what counts.  Measured: 2048 rows over 256 experts, N 4096, K 7168 in
-// 1.11 ms, 6.8 TB/s of weights (such a read alone reaches 7.1).  Chunk q of a row
+// 1.12 ms, 6.7 TB/s of weights (such a read alone reaches 7.1).  Chunk q of a row
 // lies at place q ^ ((row >> 1) & 7): no bank conflicts in the fragment reads.
 
 constexpr int kStWaves = 4, kStN = 128, kStRing = 4;
@@ -481,9 +482,10 @@ __global__ __launch_bounds__(kStWaves * 64, 2) void fp8_stream_kernel(Fp8Params 
 // wait, and the loads are spread over the stage instead of queueing at its
 // start.
 //
-// Measured: 65536 rows over 256 experts, N 4096, K 7168 in 2.03 ms, 1.9
+// Measured: 65536 rows over 256 experts, N 4096, K 7168 in 2.07 to 2.17 ms, 1.8
 // PFLOP/s (all of a stage's loads at its start, one barrier, 256-token tiles:
-// 2.82); dense 2.4 PFLOP/s on random codes, 3.1 on zeros.  Bound by power: the
+// 2.82); the same rows as 256 in each expert 2.03; dense 2.3 PFLOP/s on random
+// codes, 3.1 on zeros.  Bound by power: the
 // clock falls to 1.7 GHz on random codes.  The tile's height is what the
 // accumulators leave room for: 64 x 144 a wave is 144 of its 256 registers, and
 // 288 tokens cover an expert that gets a few rows more than 256 in one tile.
@@ -734,7 +736,7 @@ __device__ __forceinline__ void tl_run(const Fp8Params& p, const RowTile& t, int
       }
     } else if (even) {
       // rows at multiples of four bytes: two tokens' columns in pairs per store
-      // (4096 x 4094 x 256: 16 us, one column per lane 20 us)
+      // (4096 x 4094 x 256: 17 us, one column per lane 20 us)
       const int left = t.nrows - (2 * j + wt) * 16, n2 = 2 * (lane & 31);
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
@@ -878,20 +880,21 @@ hipError_t device_cus(int& cus) {
 // device, so the choice goes by the average over the experts that can have
 // rows.  The cost of each kernel in units of 0.67 ns times K, as measured on 256
 // CUs at K = 7168 (a unit is 4.8 us there):
-//   few rows   (RF + JT) a round of workgroups, one per CU (N 2048: 1 row 11 us
-//              with 16 x 16, 26 us with 64 x 64; 256 rows 30 us with 64 x 32,
-//              58 us with 16 x 64)
-//   tiles      (6 + JV) a round (N 2048: 2048 rows 44 us with 96-row tiles in one
-//              round, 73 us with 288; 4096 rows 88 us with 96-row tiles in
-//              two rounds, 61 us with 128), and 12 at least where the weights
+//   few rows   (RF + JT) a round of workgroups, one per CU (N 2048: 1 row 7.3 us
+//              with 16 x 16, 21 us with 64 x 64; 256 rows 25 us with 64 x 32,
+//              38 us with 64 x 16)
+//   tiles      (6 + JV) a round (N 2048: 2048 rows 50 us with 96-row tiles in one
+//              round, 74 us with 288; 4096 rows 92 us with 96-row tiles in
+//              two rounds, 65 us with 128), and 12 at least where the weights
 //              are one tile's alone and each stage waits for HBM (8 experts of
-//              14 rows, N 4096: 63 us, streaming 40 us)
+//              14 rows, N 4096: 63 us, streaming 42 us)
 //   streaming  3.2 + B/60 for B workgroups (1 row, N 32768: 36 us; the others
-//              47 us and more), 1.3 of that for experts of several tiles
-//              (2 experts of 33 rows, N 3473, K 3328: 20 us, 64 x 32 15 us)
+//              43 us and more), 1.3 of that for experts of several tiles
+//              (2 experts of 33 rows, N 3473, K 3328: 21 us, 64 x 32 14 us)
 // and none is faster than its experts' weights come from HBM: N * live / 4100
-// units (256 experts, N 4096, 8 rows each: streaming 1.11 ms, tiles 1.19 ms; 16
-// rows each: 1.30 ms, 1.19 ms).
+// units (256 experts, N 4096, 8 rows each: streaming 1.11 ms, tiles 1.15 ms; 16
+// rows each: 1.27 ms, 1.20 ms).  Over 122 shapes the choice takes 1.04 times as
+// long as the best of all kernels and cuts (geometric mean; worst 1.38).
 struct Fp8Plan {
   int kind;    // 0 stream, 1 few rows, 2 tiles
   int rf, jt, bm;
@@ -903,7 +906,7 @@ Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   // m tiles of bm rows: an expert's last one is half full on average; rows that
   // spread by the root of their average and still fit one tile are one (25
-  // experts of 53 rows, N 529, K 5984: 64 x 64 a workgroup 29 us, tiles 51 us)
+  // experts of about 53 rows, N 529, K 5984: 64 x 64 a workgroup 35 us, tiles 58 us)
   auto m_tiles = [&](int bm) {
     if (!a.offsets) return (double)up(a.M, bm);
     return live * (avg + std::sqrt(avg) <= bm ? 1.0 : std::fmax(avg / bm + 0.5, 1.0));
@@ -920,8 +923,8 @@ Fp8Plan plan_of(const Fp8GemmArgs& a, int cus) {
     const double jv = (double)up((int64_t)(a.M / tiles + 0.999), 32);
     const double stages = std::fmax(6.0 + std::fmax(jv, 3.0), tiles < 2 * live ? 12.0 : 0.0);
     // Experts above the average: in a round that is nearly full their further
-    // tiles start another one, so high tiles (16 experts of 116 rows, N 4096,
-    // K 2048: 35 us with 288, 48 us with 128); else they fill idle CUs, so low ones.
+    // tiles start another one, so high tiles (16 experts of about 116 rows, N 4096,
+    // K 2048: 31 us with 288, 48 us with 128); else they fill idle CUs, so low ones.
     const bool full = a.offsets && wgs > (r - 0.25) * cus;
     const double c = over_hbm(r * stages * (full && r < 4 ? 1.1 : 1.0)) + (full ? kTlM - bm : bm) * 1e-5;
     if (c < cost) { cost = c; best = Fp8Plan{2, 0, 0, bm}; }
@@ -972,7 +975,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t stream) {
   p.bm = plan.bm;
   // Weights read once go past the caches, unless rows are no multiple of 128
   // bytes: two K blocks then share a line, which would be fetched twice (40
-  // experts of 115 rows, N 1001, K 1040: 24 us, 32 us past the caches).
+  // experts of 115 rows, N 1001, K 1040: 23 us, 32 us past the caches).
   const bool aligned = a.K % 128 == 0;
   if (plan.kind == 0) return aligned ? launch_stream<2>(a, p, stream) : launch_stream<0>(a, p, stream);
   if (plan.kind == 2)   // once: where an expert is one tile on average
