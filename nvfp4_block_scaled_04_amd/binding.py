@@ -527,6 +527,12 @@ def _is(t, dtype, name, shape=None):
     return _dev(t, dtype, name, shape)
 
 
+def _int32(v, name):
+    """v for a C int argument, which would take a longer one's low bits."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits (got {v})")
+
+
 def _call(name, tensors, *args):
     """Call entry point `name` with `args` and the current stream of the device
     that holds the tensors (all on one device), with that device current."""
@@ -559,6 +565,7 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
     """Gradient of router_topk's weights with respect to the logits: topk_ids
     (T, k) int32, topk_w (T, k) float32 as router_topk returned them, dw (T, k)
     float32 -> dlogits (T, E) float32 (zero for experts not chosen)."""
+    _int32(E, "E")
     _is(topk_ids, torch.int32, "topk_ids")
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be 2-D")
@@ -574,6 +581,7 @@ def router_topk_bwd(topk_ids, topk_w, dw, E, out=None):
 def moe_dispatch(x, inv_perm, offsets, k, out=None):
     """x (T, H) bf16 -> rows (T*k, H) bf16 in expert order: row inv_perm[t*k+j]
     is token t; rows from offsets[E] on (invalid expert ids) are zero."""
+    _int32(k, "k")
     _is(x, torch.bfloat16, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
@@ -589,6 +597,7 @@ def moe_dispatch(x, inv_perm, offsets, k, out=None):
 def moe_dispatch_bwd(drows, inv_perm, offsets, k, out=None):
     """Gradient of moe_dispatch: drows (T*k, H) bf16 -> dx (T, H) bf16, each
     token's routed row gradients summed in fp32."""
+    _int32(k, "k")
     _is(drows, torch.bfloat16, "drows")
     if drows.dim() != 2 or k < 1 or drows.shape[0] % k:
         raise ValueError("drows must be 2-D with T*k rows")
@@ -690,6 +699,7 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
     row d; rows from offsets[E] on are not written.  offsets None: a dense
     product with one expert.  M: rows of c (default: the length of a_row_src, or
     R)."""
+    _int32(a_row_div, "a_row_div")
     _is(a, FP8, "a")
     _is(b, FP8, "b")
     if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[2]:

@@ -145,3 +145,18 @@ def test_bindings_reject_host_tensors():
                  lambda: nv.router_topk_bwd(i32[None], f32, f32, 4)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("v", [1 << 31, (1 << 32) + 1, -(1 << 31) - 1, (1 << 32) + 3])
+def test_bindings_reject_counts_beyond_32_bits(v):
+    """A count that C's int cannot hold is refused, not cut to its low bits
+    (2^32 + 1 rows a source row would read as 1)."""
+    import nvfp4_block_scaled_04_amd as nv
+    bf, f32, i32 = torch.zeros((2, 16), dtype=torch.bfloat16), torch.zeros((2, 1)), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros((2, 16), dtype=torch.float8_e4m3fn)
+    for name, call in (("a_row_div", lambda: nv.fp8_grouped_gemm(q, f32, q[None], f32[None], a_row_src=i32, a_row_div=v)),
+                       ("k", lambda: nv.moe_dispatch(bf, i32, i32, v)),
+                       ("k", lambda: nv.moe_dispatch_bwd(bf, i32, i32, v)),
+                       ("E", lambda: nv.router_topk_bwd(i32[None], f32, f32, v))):
+        with pytest.raises(ValueError, match=f"{name} .* 32 bits"):
+            call()
