@@ -528,7 +528,7 @@ def _is(t, dtype, name, shape=None):
 
 
 def _int32(v, name):
-    """v for a C int argument, which would take a longer one's low bits."""
+    """Refuse a v of which a C int argument would take the low bits only."""
     if not -(1 << 31) <= v < 1 << 31:
         raise ValueError(f"{name} must fit 32 bits (got {v})")
 
