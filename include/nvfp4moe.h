@@ -92,7 +92,8 @@ nvfp4_status nvfp4_weight_layout(const void* src_bf16, int64_t groups, int64_t r
  * Outputs: q uint8 [groups*rows][cols/2], sf uint8 [groups*rows][cols/16],
  *   gs_out float [groups] (all device).
  * Shapes: groups >= 0, rows_per_group >= 0, cols >= 16, cols % 16 == 0,
- *   ld_x >= cols, ld_x % 8 == 0 (else NVFP4_ERR_SHAPE).
+ *   ld_x >= cols, ld_x % 8 == 0; with gs_in or several groups fewer than
+ *   2^36 - 4096 elements (else NVFP4_ERR_SHAPE).
  * Workspace: nvfp4_quantize_workspace_size() bytes (0 allowed with NULL).
  * ---------------------------------------------------------------------- */
 size_t nvfp4_quantize_workspace_size(int64_t groups, int64_t rows_per_group, int64_t cols);

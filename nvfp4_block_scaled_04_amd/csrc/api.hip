@@ -235,6 +235,10 @@ nvfp4_status nvfp4_quantize(const void* x, int64_t groups, int64_t rows_per_grou
                             float* gs_out, void* ws, size_t ws_bytes, void* stream) {
   nvfp4_status st = check_quantize(x, groups, rows_per_group, cols, ld_x, q, sf, gs_out);
   if (st != NVFP4_OK) return st;
+  // a thread per block of 16, and a launch of 2^32 threads or more would wrap
+  // without an error (one group whose scale is computed goes grid-stride)
+  if ((gs_in != nullptr || groups > 1) && groups * rows_per_group * (cols / 16) >= (int64_t(1) << 32) - 256)
+    return fail(NVFP4_ERR_SHAPE, "several groups, or given scales, must hold fewer than 2^36 - 4096 elements");
   if (gs_in == nullptr) {
     const size_t need = nvfp4_quantize_workspace_size(groups, rows_per_group, cols);
     if (need > 0 && (ws == nullptr || ws_bytes < need))

@@ -225,3 +225,12 @@ def test_noalloc_forward_rejects_before_touching_the_device(L):
     assert b"static scratch" in L.nvfp4_last_error()
     assert f(H=200) == -2
     assert f(gs_h=None) == -1
+
+
+@pytest.mark.parametrize("groups,gs_in", [(2, None), (1, FAKE), (4, FAKE)])
+def test_quantize_rejects_more_blocks_than_a_launch_holds(L, groups, gs_in):
+    """2^32 blocks of 16 in several groups, or with given scales, take a thread
+    each: more than one launch holds."""
+    args = (FAKE, groups, (1 << 22) // groups, 1 << 14, 1 << 14, gs_in, FAKE, FAKE, FAKE, FAKE, 1 << 20, None)
+    assert L.nvfp4_quantize(*args) == -2
+    assert b"2^36" in L.nvfp4_last_error()
