@@ -530,6 +530,77 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64
                                     int64_t K, const uint8_t* b_q, const float* b_sf, void* c_bf16,
                                     void* stream);
 
+/* ------------------------------------------------------------------------
+ * RMS norm with the residual's addition, BF16 and FP8 outputs; its gradient.
+ * What the router and the expert products read.
+ *
+ * nvfp4_rmsnorm, a row at a time, sums in fp32:
+ *   h = bf16_rne(x + residual)   (residual == NULL: h is x and is not written),
+ *   rstd = 1 / sqrt(mean of h^2 + eps),   v = h * rstd * w  (fp32),
+ *   y = bf16_rne(v);  q, sf: v in FP8 as nvfp4_fp8_quantize makes it (v itself,
+ *   not y).
+ * The norm is of the stored h.  Rows of x and residual are ld_x and ld_r
+ * elements apart; h, y BF16 [rows][cols], q uint8 [rows][cols], sf float
+ * [rows][ceil(cols/128)], rstd float [rows] (for the gradient); w float
+ * (w_fp32 = 1) or BF16 (0) [cols].  y, the pair q and sf, and rstd are each
+ * nullable, but one of y and q is needed.  h may be x or residual itself
+ * (rows contiguous).  Rows whose mean of h^2 passes the largest fp32 give 0.
+ * Shapes: rows in [0, 2^31); cols % 8 == 0 (with q: % 16), 8 <= cols <= 32768;
+ *   ld_x, ld_r >= cols and multiples of 8; eps > 0.  No workspace.
+ *
+ * nvfp4_rmsnorm_bwd: dy the gradient of v (of y, or straight through the FP8
+ * rounding), dh (nullable) that of h from elsewhere, h and rstd as the forward
+ * made them (h: x without a residual).  With n = h * rstd and g = dy * w:
+ *   dx = bf16_rne( dh + rstd * (g - n * mean of g*n) ), the gradient of x and of
+ *        residual alike;
+ *   dw = sum over rows of dy * n  (fp32, nullable).
+ * dy, dh, h, dx BF16 [rows][cols], contiguous; dw float [cols], zero for no
+ * rows.  dx may be dy or dh itself.  Every sum has a fixed order: equal inputs
+ * give equal bits.
+ * Workspace: with dw nvfp4_rmsnorm_bwd_workspace_size() bytes, 16-byte aligned.
+ * Outputs must not overlap inputs otherwise, nor each other.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_rmsnorm(const void* x_bf16, int64_t ld_x, const void* residual_bf16, int64_t ld_r,
+                           const void* w, int w_fp32, int64_t rows, int64_t cols, float eps,
+                           void* h_bf16, void* y_bf16, uint8_t* q, float* sf, float* rstd, void* stream);
+size_t nvfp4_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols);
+nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const void* h_bf16,
+                               const float* rstd, const void* w, int w_fp32, int64_t rows, int64_t cols,
+                               void* dx_bf16, float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The expert layer for a few tokens, in two kernels.
+ * For serving steps of up to NVFP4_FEW_TOKENS tokens, where the weights' bytes
+ * bound the layer: activations are not quantised.  With e = topk_ids[t][j]:
+ *   [gate | up] = W1[e] x[t],   h = silu(gate) * up   (fp32),
+ *   out[t] = bf16_rne( sum_j topk_w[t][j] * W2[e] h ),
+ * products and sums in fp32, each h rounded to 16 bits of significand.  Ids
+ * outside [0, E) contribute nothing (a token with none but these gives zeros);
+ * an id may come twice in a row.  A shared expert is a further expert and a
+ * further slot of weight 1.  Each live expert's weights are read once.
+ * x, out BF16 [T][H]; topk_ids int32, topk_w float [T][k].
+ * moe_expert_forward_few: the weights of moe_expert_forward (w1 interleaved,
+ *   packed by nvfp4_pack_weights; E2M1 * E4M3 / gs).
+ * moe_expert_forward_few_fp8: w1 [E][2I][H] ([gate | up] rows), w2 [E][H][I]
+ *   with their scales, as nvfp4_fp8_quantize_weight makes them.
+ * Shapes: 0 <= T <= NVFP4_FEW_TOKENS, 1 <= k <= 64, 1 <= E <= 4096; H and I
+ *   multiples of 128 (FP8: 16), below 2^20, 2*I*H < 2^31.
+ * Workspace: moe_expert_forward_few_workspace_size() bytes, 16-byte aligned;
+ *   nothing in it needs a value beforehand.  Calls that share one must be
+ *   ordered on one stream.  Outputs must not overlap inputs.
+ * ---------------------------------------------------------------------- */
+#define NVFP4_FEW_TOKENS 16
+size_t moe_expert_forward_few_workspace_size(int64_t T, int64_t I, int k);
+nvfp4_status moe_expert_forward_few(const void* x_bf16, int64_t T, int64_t H, int64_t I, int E, int k,
+                                    const int32_t* topk_ids, const float* topk_w, const uint8_t* w1_q,
+                                    const uint8_t* w1_sf, const float* gs_w1, const uint8_t* w2_q,
+                                    const uint8_t* w2_sf, const float* gs_w2, void* out_bf16, void* ws,
+                                    size_t ws_bytes, void* stream);
+nvfp4_status moe_expert_forward_few_fp8(const void* x_bf16, int64_t T, int64_t H, int64_t I, int E, int k,
+                                        const int32_t* topk_ids, const float* topk_w, const uint8_t* w1_q,
+                                        const float* w1_sf, const uint8_t* w2_q, const float* w2_sf,
+                                        void* out_bf16, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,8 @@ from .binding import (  # noqa: F401
     prepare_expert_weights, quantize, quantize_scatter, router_topk, to_mx, weight_layout,
     fp8_grouped_gemm, fp8_quantize, fp8_quantize_weight, fp8_swiglu_quantize, moe_combine_bwd,
     moe_dispatch, moe_dispatch_bwd, router_topk_bwd,
+    FEW_TOKENS, few_workspace, fp8_rmsnorm, moe_expert_forward_few, moe_expert_forward_few_fp8, rmsnorm,
+    rmsnorm_bwd,
 )
 
 __version__ = "0.1.0"

@@ -70,6 +70,19 @@ SIGNATURES = {
     "nvfp4_fp8_grouped_gemm": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int,
                                        c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                        c_void_p]),
+    "nvfp4_rmsnorm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_int64, c_int64,
+                              ctypes.c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_void_p]),
+    "nvfp4_rmsnorm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "nvfp4_rmsnorm_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int64,
+                                  c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_expert_forward_few_workspace_size": (c_size_t, [c_int64, c_int64, c_int]),
+    "moe_expert_forward_few": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_int, c_int, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_expert_forward_few_fp8": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_int, c_int, c_void_p,
+                                           c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                           c_void_p, c_size_t, c_void_p]),
 }
 SIGNATURES["nvfp4_moe_dispatch_bwd"] = SIGNATURES["nvfp4_moe_dispatch"]
 SIGNATURES["nvfp4_fp8_swiglu_quantize"] = SIGNATURES["nvfp4_fp8_quantize"]
@@ -723,3 +736,165 @@ def fp8_grouped_gemm(a, a_sf, b, b_sf, offsets=None, M=None, a_row_src=None, a_r
     _call("nvfp4_fp8_grouped_gemm", (a, a_sf, b, b_sf, offsets, a_row_src, c), _ptr(a), _ptr(a_sf), R,
           _ptr(a_row_src), a_row_div, _ptr(offsets), E, M, N, K, _ptr(b), _ptr(b_sf), _ptr(c))
     return c
+
+
+# ------------------------------------------------------------------ RMS norm, expert layer for a few tokens
+
+FEW_TOKENS = 16      # NVFP4_FEW_TOKENS
+
+
+def _ld(x):
+    """Row stride of a 2-D x; a one-row tensor's is arbitrary."""
+    return x.stride(0) if x.shape[0] > 1 else (x.shape[1] + 7) // 8 * 8
+
+
+def _rows_of(t, name):
+    """A 2-D BF16 tensor whose rows may be spaced apart."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.dim() == 2
+            and t.is_contiguous()):
+        _dev(t, torch.bfloat16, name, rows=True)
+
+
+def _norm_weight(w, H):
+    if isinstance(w, torch.Tensor) and w.dtype is torch.float32:
+        _is(w, torch.float32, "w", (H,))
+        return 1
+    _is(w, torch.bfloat16, "w", (H,))
+    return 0
+
+
+def _rmsnorm(x, w, residual, eps, y, q, sf, h, rstd, need_y, need_q, need_rstd):
+    _rows_of(x, "x")
+    T, H = x.shape
+    wide = _norm_weight(w, H)
+    if residual is not None:
+        _rows_of(residual, "residual")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have shape {(T, H)} (got {tuple(residual.shape)})")
+        h = _out(h, (T, H), torch.bfloat16, x, "h")
+    elif h is not None:
+        raise ValueError("h is x without a residual: no tensor to write it to")
+    y = _out(y, (T, H), torch.bfloat16, x, "y") if need_y else None
+    if need_q:
+        q = _out(q, (T, H), FP8, x, "q")
+        sf = _out(sf, (T, _scale_blocks(H)), torch.float32, x, "sf")
+    rstd = _out(rstd, (T,), torch.float32, x, "rstd") if need_rstd else None
+    _call("nvfp4_rmsnorm", (x, residual, w, h, y, q, sf, rstd), _ptr(x), _ld(x), _ptr(residual),
+          _ld(residual) if residual is not None else 0, _ptr(w), wide, T, H, eps, _ptr(h), _ptr(y), _ptr(q),
+          _ptr(sf), _ptr(rstd))
+    return y, q, sf, x if residual is None else h, rstd
+
+
+def rmsnorm(x, w, residual=None, eps=1e-6, need_rstd=False, out=None):
+    """RMS norm of h = x + residual (rounded to bf16; h is x without a residual):
+    y = h / sqrt(mean(h^2) + eps) * w.  x, residual (T, H) bf16, rows may be
+    spaced apart; w (H,) bf16 or float32 -> (y (T, H) bf16, h (T, H) bf16, rstd
+    (T,) float32 or None).  out: (y, h, rstd) tensors to write, None for one to
+    be made; h may be residual (or x) itself."""
+    y, h, rstd = out if out is not None else (None, None, None)
+    y, _, _, h, rstd = _rmsnorm(x, w, residual, eps, y, None, None, h, rstd, True, False,
+                                need_rstd or rstd is not None)
+    return y, h, rstd
+
+
+def fp8_rmsnorm(x, w, residual=None, eps=1e-6, need_y=False, need_rstd=False, out=None):
+    """rmsnorm with the normalised rows in FP8, as fp8_quantize of the unrounded
+    values would make them -> (q (T, H) float8_e4m3fn, sf (T, ceil(H/128))
+    float32, y (T, H) bf16 or None, h (T, H) bf16, rstd (T,) float32 or None).
+    out: (q, sf, y, h, rstd) tensors to write, None for one to be made."""
+    q, sf, y, h, rstd = out if out is not None else (None,) * 5
+    y, q, sf, h, rstd = _rmsnorm(x, w, residual, eps, y, q, sf, h, rstd, need_y or y is not None, True,
+                                 need_rstd or rstd is not None)
+    return q, sf, y, h, rstd
+
+
+def rmsnorm_bwd(dy, h, w, rstd, dh=None, need_dw=True, out=None, workspace=None):
+    """Gradient of rmsnorm and fp8_rmsnorm: dy (T, H) bf16 the gradient of the
+    normalised rows, h and rstd as they returned them, dh (T, H) bf16 the gradient
+    that reaches h from elsewhere -> (dx (T, H) bf16, of x and residual alike,
+    dw (H,) float32 or None).  out: (dx, dw) tensors to write; dx may be dy or dh.
+    workspace: uint8 tensor of nvfp4_rmsnorm_bwd_workspace_size(T, H) bytes."""
+    _is(dy, torch.bfloat16, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    T, H = dy.shape
+    _is(h, torch.bfloat16, "h", (T, H))
+    wide = _norm_weight(w, H)
+    _is(rstd, torch.float32, "rstd", (T,))
+    if dh is not None:
+        _is(dh, torch.bfloat16, "dh", (T, H))
+    dx, dw = out if out is not None else (None, None)
+    dx = _out(dx, (T, H), torch.bfloat16, dy, "dx")
+    ws = None
+    if need_dw:
+        dw = _out(dw, (H,), torch.float32, dy, "dw")
+        ws = workspace
+        if ws is None:
+            ws = _workspace(lib().nvfp4_rmsnorm_bwd_workspace_size(T, H), dy.device)
+        _is(ws, torch.uint8, "workspace")
+    else:
+        dw = None
+    _call("nvfp4_rmsnorm_bwd", (dy, dh, h, rstd, w, dx, dw, ws), _ptr(dy), _ptr(dh), _ptr(h), _ptr(rstd), _ptr(w),
+          wide, T, H, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() if ws is not None else 0)
+    return dx, dw
+
+
+def _few(name, x, topk_ids, topk_w, H, I, E, weights, out, workspace):
+    _is(x, torch.bfloat16, "x")
+    if x.dim() != 2 or not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("x and topk_ids must be 2-D")
+    T, k = x.shape[0], topk_ids.shape[1]
+    if x.shape[1] != H:
+        raise ValueError("weight shapes do not match x")
+    _is(topk_ids, torch.int32, "topk_ids", (T, k))
+    _is(topk_w, torch.float32, "topk_w", (T, k))
+    o = _out(out, (T, H), torch.bfloat16, x)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(lib().moe_expert_forward_few_workspace_size(T, I, k), x.device)
+    _is(ws, torch.uint8, "workspace")
+    _call(name, (x, topk_ids, topk_w, *weights, o, ws), _ptr(x), T, H, I, E, k, _ptr(topk_ids), _ptr(topk_w),
+          *[t.data_ptr() for t in weights], _ptr(o), _ptr(ws), ws.numel())
+    return o
+
+
+def few_workspace(T, I, k, device):
+    """Workspace of the two calls below."""
+    return _workspace(lib().moe_expert_forward_few_workspace_size(T, I, k), device)
+
+
+def moe_expert_forward_few(x, topk_ids, topk_w, w: ExpertWeights, out=None, workspace=None):
+    """The expert layer for at most FEW_TOKENS tokens in two kernels, activations
+    not quantised: x (T, H) bf16, topk_ids (T, k) int32, topk_w (T, k) float32 and
+    the NVFP4 weights of moe_expert_forward -> out (T, H) bf16."""
+    if w.mx:
+        raise ValueError("the forward for a few tokens takes the NVFP4 weights")
+    E, H, I = w.E, w.H, w.I
+    if w.w2.N != H or w.w2.K != I or w.w2.E != E:
+        raise ValueError("weight shapes do not match")
+    L = lib()
+    sf = c_size_t(0)
+    for p, name in ((w.w1, "w1"), (w.w2, "w2")):
+        _is(p.q, torch.uint8, name + ".q")
+        _is(p.sf, torch.uint8, name + ".sf")
+        if p.q.numel() < L.nvfp4_packed_weight_bytes(E, p.N, p.K, ctypes.byref(sf)) or p.sf.numel() < sf.value:
+            raise ValueError(f"{name} holds less than its packed experts")
+    _is(w.gs_w1, torch.float32, "gs_w1", (E,))
+    _is(w.gs_w2, torch.float32, "gs_w2", (E,))
+    return _few("moe_expert_forward_few", x, topk_ids, topk_w, H, I, E,
+                (w.w1.q, w.w1.sf, w.gs_w1, w.w2.q, w.w2.sf, w.gs_w2), out, workspace)
+
+
+def moe_expert_forward_few_fp8(x, topk_ids, topk_w, w1, w1_sf, w2, w2_sf, out=None, workspace=None):
+    """moe_expert_forward_few with FP8 experts: w1 (E, 2I, H) and w2 (E, H, I)
+    float8_e4m3fn, rows of w1 [gate | up], with their scales from
+    fp8_quantize_weight."""
+    _is(w1, FP8, "w1")
+    _is(w2, FP8, "w2")
+    if w1.dim() != 3 or w2.dim() != 3 or w1.shape[0] != w2.shape[0] or w1.shape[1] != 2 * w2.shape[2] \
+            or w1.shape[2] != w2.shape[1]:
+        raise ValueError("w1 must be (E, 2I, H) and w2 (E, H, I)")
+    E, H, I = w2.shape
+    _is(w1_sf, torch.float32, "w1_sf", (E, _scale_blocks(2 * I), _scale_blocks(H)))
+    _is(w2_sf, torch.float32, "w2_sf", (E, _scale_blocks(H), _scale_blocks(I)))
+    return _few("moe_expert_forward_few_fp8", x, topk_ids, topk_w, H, I, E, (w1, w1_sf, w2, w2_sf), out, workspace)

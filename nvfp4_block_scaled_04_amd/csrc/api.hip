@@ -848,3 +848,195 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- RMS norm, expert layer for a few tokens
+namespace {
+
+constexpr int64_t kNormMaxCols = 32768;
+
+nvfp4_status check_norm(int64_t rows, int64_t cols, float eps) {
+  if (rows < 0 || rows >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "rows must be in [0, 2^31)");
+  if (cols < 8 || cols % 8 || cols > kNormMaxCols)
+    return fail(NVFP4_ERR_SHAPE, "cols must be a positive multiple of 8 up to %lld (got %lld)",
+                (long long)kNormMaxCols, (long long)cols);
+  if (!(eps > 0.0f) || eps > 3.0e38f) return fail(NVFP4_ERR_INVALID_ARG, "eps must be positive and finite");
+  return NVFP4_OK;
+}
+
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// does any output (nullptr: absent) overlap an input or another output?
+template <size_t N, size_t M>
+bool any_overlap(const Span (&out)[N], const Span (&in)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    if (!out[i].p) continue;
+    for (size_t j = 0; j < M; ++j)
+      if (in[j].p && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (size_t j = i + 1; j < N; ++j)
+      if (out[j].p && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+nvfp4_status few_impl(bool fp8, const char* what, const void* x, int64_t T, int64_t H, int64_t I, int E, int k,
+                      const int32_t* ids, const float* topk_w, const uint8_t* w1_q, const void* w1_sf,
+                      const float* gs_w1, const uint8_t* w2_q, const void* w2_sf, const float* gs_w2, void* out,
+                      void* ws, size_t ws_bytes, void* stream) {
+  const int64_t unit = fp8 ? 16 : 128;
+  if (T < 0 || T > NVFP4_FEW_TOKENS)
+    return fail(NVFP4_ERR_SHAPE, "T must be in [0, %d] (got %lld)", NVFP4_FEW_TOKENS, (long long)T);
+  if (H < unit || H % unit || I < unit || I % unit || H >= (int64_t(1) << 20) || I >= (int64_t(1) << 20))
+    return fail(NVFP4_ERR_SHAPE, "H and I must be positive multiples of %lld below 2^20 (got %lld, %lld)",
+                (long long)unit, (long long)H, (long long)I);
+  if (2 * I * H >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "an expert's weight (2*I*H) must be below 2^31 elements");
+  if (E < 1 || E > 4096) return fail(NVFP4_ERR_SHAPE, "E must be in [1, 4096] (got %d)", E);
+  if (k < 1 || k > 64) return fail(NVFP4_ERR_SHAPE, "k must be in [1, 64] (got %d)", k);
+  if (T == 0) return NVFP4_OK;
+  if (!x || !ids || !topk_w || !w1_q || !w1_sf || !w2_q || !w2_sf || !out || (!fp8 && (!gs_w1 || !gs_w2)))
+    return fail(NVFP4_ERR_INVALID_ARG, "x, topk_ids, topk_w, the weights, their scales and out must be non-NULL");
+  if (!aligned(x, 16) || !aligned(w1_q, 16) || !aligned(w2_q, 16) || !aligned(w1_sf, fp8 ? 4 : 8) ||
+      !aligned(w2_sf, fp8 ? 4 : 8) || !aligned(out, 16) || !aligned(ids, 4) || !aligned(topk_w, 4) ||
+      !aligned(gs_w1, 4) || !aligned(gs_w2, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "x, codes and out must be 16-byte, NVFP4 scales 8-byte, the other arrays 4-byte aligned");
+  const size_t need = moe_expert_forward_few_workspace_size(T, I, k);
+  if (!ws || ws_bytes < need || !aligned(ws, 16))
+    return fail(NVFP4_ERR_WORKSPACE, "%s needs %zu workspace bytes, 16-byte aligned (got %zu)", what, need, ws_bytes);
+  auto codes = [&](int64_t N, int64_t K) { return E * (fp8 ? N * K : nvfp4::packed_rows(N) * (K / 2)); };
+  auto scales = [&](int64_t N, int64_t K) {
+    return E * (fp8 ? 4 * ((N + 127) / 128) * ((K + 127) / 128) : nvfp4::packed_rows(N) * (K / 16));
+  };
+  const Span outs[] = {{out, 2 * T * H}, {ws, (int64_t)need}};
+  const Span ins[] = {{x, 2 * T * H}, {ids, 4 * T * k}, {topk_w, 4 * T * k}, {w1_q, codes(2 * I, H)},
+                      {w1_sf, scales(2 * I, H)}, {w2_q, codes(H, I)}, {w2_sf, scales(H, I)},
+                      {gs_w1, 4 * (int64_t)E}, {gs_w2, 4 * (int64_t)E}};
+  if (any_overlap(outs, ins))
+    return fail(NVFP4_ERR_INVALID_ARG, "out and the workspace must not overlap the inputs or each other");
+  nvfp4_status st = check_arch();
+  if (st != NVFP4_OK) return st;
+  nvfp4::FewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.T = (int)T; a.k = k; a.E = E; a.H = H; a.I = I;
+  a.ids = ids; a.topk_w = topk_w;
+  a.fp8 = fp8;
+  a.w1_q = w1_q; a.w2_q = w2_q; a.w1_sf = w1_sf; a.w2_sf = w2_sf;
+  a.gs_w1 = gs_w1; a.gs_w2 = gs_w2;
+  a.h_hi = static_cast<uint16_t*>(ws);
+  a.h_lo = a.h_hi + T * k * I;
+  a.out = static_cast<uint16_t*>(out);
+  return finish(nvfp4::launch_few(a, static_cast<hipStream_t>(stream)), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* w,
+                           int w_fp32, int64_t rows, int64_t cols, float eps, void* h, void* y, uint8_t* q,
+                           float* sf, float* rstd, void* stream) {
+  nvfp4_status st = check_norm(rows, cols, eps);
+  if (st != NVFP4_OK) return st;
+  if (w_fp32 != 0 && w_fp32 != 1) return fail(NVFP4_ERR_INVALID_ARG, "w_fp32 must be 0 or 1 (got %d)", w_fp32);
+  if (ld_x < cols || ld_x % 8 || ld_x >= (int64_t(1) << 40) ||
+      (residual && (ld_r < cols || ld_r % 8 || ld_r >= (int64_t(1) << 40))))
+    return fail(NVFP4_ERR_SHAPE, "ld_x and ld_r must be >= cols and multiples of 8");
+  if (q && cols % 16) return fail(NVFP4_ERR_SHAPE, "FP8 outputs need cols %% 16 == 0 (got %lld)", (long long)cols);
+  if (rows == 0) return NVFP4_OK;
+  if (ld_x >= (int64_t(1) << 60) / rows || (residual && ld_r >= (int64_t(1) << 60) / rows))
+    return fail(NVFP4_ERR_SHAPE, "rows * ld_x and rows * ld_r must be below 2^60");
+  if (!x || !w) return fail(NVFP4_ERR_INVALID_ARG, "x and w must be non-NULL");
+  if (!y && !q) return fail(NVFP4_ERR_INVALID_ARG, "one of y and q must be non-NULL");
+  if ((residual != nullptr) != (h != nullptr))
+    return fail(NVFP4_ERR_INVALID_ARG, "h is written with a residual, and only then");
+  if ((q != nullptr) != (sf != nullptr)) return fail(NVFP4_ERR_INVALID_ARG, "q and sf must be given together");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(w, 16) || !aligned(h, 16) || !aligned(y, 16) ||
+      !aligned(q, 8) || !aligned(sf, 4) || !aligned(rstd, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "x, residual, w, h and y must be 16-byte, q 8-byte, sf and rstd 4-byte aligned");
+  const int64_t xb = 2 * ((rows - 1) * ld_x + cols), rb = 2 * ((rows - 1) * ld_r + cols), n = rows * cols;
+  const Span outs[] = {{h, 2 * n}, {y, 2 * n}, {q, n}, {sf, 4 * rows * ((cols + 127) / 128)}, {rstd, 4 * rows}};
+  // h may be x or the residual itself, rows in their places
+  const Span ins[] = {{h && h == x && ld_x == cols ? nullptr : x, xb},
+                      {h && h == residual && ld_r == cols ? nullptr : residual, rb},
+                      {w, (w_fp32 ? 4 : 2) * cols}};
+  if (any_overlap(outs, ins))
+    return fail(NVFP4_ERR_INVALID_ARG, "outputs must not overlap the inputs (but h may be x or residual) or each other");
+  st = check_arch();
+  if (st != NVFP4_OK) return st;
+  nvfp4::RmsnormArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ld_x = ld_x; a.ld_r = residual ? ld_r : 0; a.rows = rows; a.cols = (int)cols; a.eps = eps;
+  a.w = w; a.wide = w_fp32 != 0;
+  a.h = static_cast<uint16_t*>(h);
+  a.y = static_cast<uint16_t*>(y);
+  a.q = q; a.sf = sf; a.rstd = rstd;
+  return finish(nvfp4::launch_rmsnorm(a, static_cast<hipStream_t>(stream)), "nvfp4_rmsnorm launch");
+}
+
+size_t nvfp4_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 8 || cols > kNormMaxCols) return 0;
+  return sizeof(float) * (size_t)nvfp4::rmsnorm_bwd_groups(rows, cols) * (size_t)cols;
+}
+
+nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const float* rstd, const void* w,
+                               int w_fp32, int64_t rows, int64_t cols, void* dx, float* dw, void* ws,
+                               size_t ws_bytes, void* stream) {
+  nvfp4_status st = check_norm(rows, cols, 1.0f);
+  if (st != NVFP4_OK) return st;
+  if (w_fp32 != 0 && w_fp32 != 1) return fail(NVFP4_ERR_INVALID_ARG, "w_fp32 must be 0 or 1 (got %d)", w_fp32);
+  if (rows == 0 && !dw) return NVFP4_OK;
+  if (rows > 0 && (!dy || !h || !rstd || !w || !dx))
+    return fail(NVFP4_ERR_INVALID_ARG, "dy, h, rstd, w and dx must be non-NULL");
+  if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
+      !aligned(rstd, 4) || !aligned(dw, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "dy, dh, h, w and dx must be 16-byte, rstd and dw 4-byte aligned");
+  const size_t need = dw ? nvfp4_rmsnorm_bwd_workspace_size(rows, cols) : 0;
+  if (dw && (!ws || ws_bytes < need || !aligned(ws, 16)))
+    return fail(NVFP4_ERR_WORKSPACE, "nvfp4_rmsnorm_bwd needs %zu workspace bytes, 16-byte aligned (got %zu)", need, ws_bytes);
+  const int64_t n = 2 * rows * cols;
+  // dx may be dy or dh, rows in their places
+  const Span outs[] = {{dx, n}, {dw, 4 * cols}, {dw ? ws : nullptr, (int64_t)need}};
+  const Span ins[] = {{dy == dx ? nullptr : dy, n}, {dh == dx ? nullptr : dh, n}, {h, n}, {rstd, 4 * rows},
+                      {w, (w_fp32 ? 4 : 2) * cols}};
+  if (rows > 0 && any_overlap(outs, ins))
+    return fail(NVFP4_ERR_INVALID_ARG, "outputs and workspace must not overlap the inputs (but dx may be dy or dh) or each other");
+  if (rows > 0 && ((dy == dx && dw && overlap(dw, 4 * cols, dy, n)) || (dh && dh == dx && dw && overlap(dw, 4 * cols, dh, n))))
+    return fail(NVFP4_ERR_INVALID_ARG, "dw must not overlap the inputs");
+  st = check_arch();
+  if (st != NVFP4_OK) return st;
+  nvfp4::RmsnormBwdArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dh = static_cast<const uint16_t*>(dh);
+  a.h = static_cast<const uint16_t*>(h);
+  a.rstd = rstd; a.w = w; a.wide = w_fp32 != 0; a.rows = rows; a.cols = (int)cols;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.part = dw ? static_cast<float*>(ws) : nullptr;
+  a.dw = dw;
+  return finish(nvfp4::launch_rmsnorm_bwd(a, static_cast<hipStream_t>(stream)), "nvfp4_rmsnorm_bwd launch");
+}
+
+size_t moe_expert_forward_few_workspace_size(int64_t T, int64_t I, int k) {
+  if (T <= 0 || T > NVFP4_FEW_TOKENS || I < 1 || k < 1) return 0;
+  return align256(4 * (size_t)T * (size_t)k * (size_t)I);
+}
+
+nvfp4_status moe_expert_forward_few(const void* x, int64_t T, int64_t H, int64_t I, int E, int k,
+                                    const int32_t* topk_ids, const float* topk_w, const uint8_t* w1_q,
+                                    const uint8_t* w1_sf, const float* gs_w1, const uint8_t* w2_q,
+                                    const uint8_t* w2_sf, const float* gs_w2, void* out, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  return few_impl(false, "moe_expert_forward_few", x, T, H, I, E, k, topk_ids, topk_w, w1_q, w1_sf, gs_w1, w2_q,
+                  w2_sf, gs_w2, out, ws, ws_bytes, stream);
+}
+
+nvfp4_status moe_expert_forward_few_fp8(const void* x, int64_t T, int64_t H, int64_t I, int E, int k,
+                                        const int32_t* topk_ids, const float* topk_w, const uint8_t* w1_q,
+                                        const float* w1_sf, const uint8_t* w2_q, const float* w2_sf, void* out,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  return few_impl(true, "moe_expert_forward_few_fp8", x, T, H, I, E, k, topk_ids, topk_w, w1_q, w1_sf, nullptr,
+                  w2_q, w2_sf, nullptr, out, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

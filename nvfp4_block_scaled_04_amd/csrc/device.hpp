@@ -14,6 +14,7 @@ namespace nvfp4 {
 constexpr float kUnderflow = 0.01171875f;   // 6 * 2^-9: E2M1 max * E4M3 min subnormal
 constexpr float kGsNumerator = 2688.0f;     // 448 * 6: E4M3 max * E2M1 max
 constexpr float kE4m3Max = 448.0f;
+constexpr float kFp8Floor = 7.888609052210118e-31f;   // 2^-100: smallest block maximum of the FP8 quantisers
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
@@ -59,6 +60,18 @@ __device__ __forceinline__ float e4m3_decode(uint32_t b) {
   const float sub = (float)m * 0.001953125f;   // m * 2^-9, exact
   const float nrm = __uint_as_float(((e + 120u) << 23) | (m << 20));
   return e == 0 ? sub : nrm;
+}
+
+// Eight fp32 values times r -> eight E4M3 codes (v_cvt_pk_fp8_f32 rounds to
+// nearest, ties to even); |x * r| must round to at most 448.
+__device__ __forceinline__ uint2 fp8_encode8(const float (&x)[8], float r) {
+#pragma clang fp contract(off)
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * r, x[1] * r, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * r, x[5] * r, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * r, x[7] * r, hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
 // Eight fp32 values -> eight E2M1 codes (value i in bits 4i..4i+3):

@@ -24,8 +24,6 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr float kFp8Max = 448.0f;
-constexpr float kFp8Floor = 7.888609052210118e-31f;   // 2^-100
 constexpr int kQThreads = 256;
 constexpr int kQGroups = kQThreads / 16;              // blocks of 128 per pass of a workgroup
 
@@ -41,16 +39,6 @@ __device__ __forceinline__ float max16(float m) {
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   return m;
-}
-
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float r) {
-#pragma clang fp contract(off)
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * r, x[1] * r, lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * r, x[5] * r, hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * r, x[7] * r, hi, true);
-  return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
 // silu(g) * u = (g / 4) / ((1 + exp(-g)) / 4) * u within 2^-21 of itself, far
@@ -112,8 +100,8 @@ __global__ __launch_bounds__(kQThreads) void fp8_rows_kernel(
     else unpack8(a[i], v);
     const float m = fmaxf(max16(amax8(v)), kFp8Floor);
     if (row0 + i < rows) {
-      if (in) *reinterpret_cast<uint2*>(q + (row0 + i) * cols + col) = encode8(v, kFp8Max / m);
-      if (l == 0) sf[(row0 + i) * kblocks + kb] = m / kFp8Max;
+      if (in) *reinterpret_cast<uint2*>(q + (row0 + i) * cols + col) = fp8_encode8(v, kE4m3Max / m);
+      if (l == 0) sf[(row0 + i) * kblocks + kb] = m / kE4m3Max;
     }
   }
 }
@@ -153,15 +141,15 @@ __global__ __launch_bounds__(kQThreads) void fp8_weight_kernel(
   __syncthreads();
   m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
   m = fmaxf(m, kFp8Floor);
-  const float r = kFp8Max / m;
+  const float r = kE4m3Max / m;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + 16 * i;
     float v[8];
     unpack8(a[i], v);
-    if (col < cols && row < rows) *reinterpret_cast<uint2*>(q + base + row * cols + col) = encode8(v, r);
+    if (col < cols && row < rows) *reinterpret_cast<uint2*>(q + base + row * cols + col) = fp8_encode8(v, r);
   }
-  if (threadIdx.x == 0) sf[unit] = m / kFp8Max;
+  if (threadIdx.x == 0) sf[unit] = m / kE4m3Max;
 }
 
 }  // namespace

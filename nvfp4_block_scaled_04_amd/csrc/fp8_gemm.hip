@@ -861,21 +861,6 @@ hipError_t launch_tile(const Fp8GemmArgs& a, Fp8Params p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-std::atomic<int> g_cus[kMaxDevices];
-
-hipError_t device_cus(int& cus) {
-  int dev = 0;
-  hipError_t err = hipGetDevice(&dev);
-  if (err != hipSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-  cus = g_cus[dev].load(std::memory_order_relaxed);
-  if (cus > 0) return hipSuccess;
-  err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (err != hipSuccess) return err;
-  g_cus[dev].store(cus, std::memory_order_relaxed);
-  return hipSuccess;
-}
-
 // Which kernel, and how it is cut.  The row counts of the experts are on the
 // device, so the choice goes by the average over the experts that can have
 // rows.  The cost of each kernel in units of 0.67 ns times K, as measured on 256

@@ -1202,6 +1202,8 @@ hipError_t current_device(int& dev) {
   return (dev >= 0 && dev < kMaxDevices) ? hipSuccess : hipErrorInvalidDevice;
 }
 
+}  // namespace
+
 hipError_t device_cus(int& cus) {
   int dev = 0;
   hipError_t err = current_device(dev);
@@ -1213,6 +1215,8 @@ hipError_t device_cus(int& cus) {
   g_cus[dev].store(cus, std::memory_order_relaxed);
   return hipSuccess;
 }
+
+namespace {
 
 constexpr int kBN = 512, kBM = 128;   // the tile of every launch but small experts
 constexpr int kBMSmall = 32;          // experts of at most 32 rows on average

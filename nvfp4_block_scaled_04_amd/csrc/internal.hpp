@@ -104,6 +104,7 @@ constexpr size_t kGemmWorkspaceBytes = 256;
 // when it would not split)
 size_t gemm_splitk_ws_bytes(int epilogue, int64_t M, int64_t N, int64_t K, int E);
 hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream);
+hipError_t device_cus(int& cus);   // compute units of the current device
 
 // mx.hip: NVFP4 (q [rows][cols/2], E4M3 sf [rows][cols/16]) -> MXFP4 codes
 // and E8M0 scales in the same shapes (each scale byte stored twice);
@@ -149,6 +150,55 @@ hipError_t launch_dispatch_bwd(const void* drows, const int32_t* inv_perm, const
 hipError_t launch_combine_bwd(const void* dout, const void* y, const int32_t* inv_perm,
                               const float* topk_w, const int32_t* offsets, int64_t T, int k, int E,
                               int64_t H, void* dy, float* dw, hipStream_t stream);
+
+// rmsnorm.hip: cols % 8 == 0, at most 32768 (FP8 outputs: cols % 16 == 0)
+struct RmsnormArgs {
+  const uint16_t* x;          // rows ld_x elements apart
+  const uint16_t* residual;   // nullable, rows ld_r apart
+  int64_t ld_x, ld_r, rows;
+  int cols;
+  float eps;
+  const void* w;              // float (wide) or BF16
+  bool wide;
+  uint16_t* h;                // written with a residual; may be x or residual
+  uint16_t* y;                // nullable
+  uint8_t* q;                 // nullable, then sf is not written
+  float* sf;
+  float* rstd;                // nullable
+};
+hipError_t launch_rmsnorm(const RmsnormArgs& a, hipStream_t stream);
+
+struct RmsnormBwdArgs {
+  const uint16_t *dy, *dh, *h;   // dh nullable
+  const float* rstd;
+  const void* w;
+  bool wide;
+  int64_t rows;
+  int cols;
+  uint16_t* dx;
+  float* part;                // rmsnorm_bwd_groups() rows of cols sums; nullptr without dw
+  float* dw;                  // nullable
+};
+int rmsnorm_bwd_groups(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, hipStream_t stream);
+
+// few.hip: the expert layer for at most kFewTokens tokens, FP8 weights
+// (row-major, one scale per 128 x 128) or packed NVFP4 weights
+constexpr int kFewTokens = NVFP4_FEW_TOKENS;
+struct FewArgs {
+  const uint16_t* x;
+  int T, k, E;
+  int64_t H, I;
+  const int32_t* ids;
+  const float* topk_w;
+  bool fp8;
+  const uint8_t *w1_q, *w2_q;
+  const void *w1_sf, *w2_sf;          // float (FP8) or E4M3 bytes
+  const float *gs_w1, *gs_w2;         // NVFP4
+  uint16_t *h_hi, *h_lo;              // [T*k][I] each: workspace
+  uint16_t* out;
+};
+hipError_t launch_few(const FewArgs& a, hipStream_t stream);
 
 // combine.hip
 hipError_t launch_combine(const void* y, const int32_t* inv_perm, const float* topk_w,

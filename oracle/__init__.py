@@ -29,4 +29,4 @@ near-tie certifier ``quantize.near_ties`` used by the GPU parity tests is
 pinned directly (values at, inside and outside the tolerance of a boundary).
 """
 
-from . import formats, quantize, route, layout, moe, mx, fp8  # noqa: F401
+from . import formats, quantize, route, layout, moe, mx, fp8, norm, few  # noqa: F401
