@@ -574,7 +574,8 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const v
  * bound the layer: activations are not quantised.  With e = topk_ids[t][j]:
  *   [gate | up] = W1[e] x[t],   h = silu(gate) * up   (fp32),
  *   out[t] = bf16_rne( sum_j topk_w[t][j] * W2[e] h ),
- * products and sums in fp32, each h rounded to 16 bits of significand.  Ids
+ * products and sums in fp32, each h rounded to 11 bits of significand or more (and
+ * to 2^-39 of the largest of 128).  Ids
  * outside [0, E) contribute nothing (a token with none but these gives zeros);
  * an id may come twice in a row.  A shared expert is a further expert and a
  * further slot of weight 1.  Each live expert's weights are read once.
@@ -584,7 +585,7 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const v
  * moe_expert_forward_few_fp8: w1 [E][2I][H] ([gate | up] rows), w2 [E][H][I]
  *   with their scales, as nvfp4_fp8_quantize_weight makes them.
  * Shapes: 0 <= T <= NVFP4_FEW_TOKENS, 1 <= k <= 64, 1 <= E <= 4096; H and I
- *   multiples of 128 (FP8: 16), below 2^20, 2*I*H < 2^31.
+ *   multiples of 128 (FP8: 16), below 2^19, 2*I*H < 2^31.
  * Workspace: moe_expert_forward_few_workspace_size() bytes, 16-byte aligned;
  *   nothing in it needs a value beforehand.  Calls that share one must be
  *   ordered on one stream.  Outputs must not overlap inputs.

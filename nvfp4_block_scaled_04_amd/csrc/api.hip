@@ -888,8 +888,8 @@ nvfp4_status few_impl(bool fp8, const char* what, const void* x, int64_t T, int6
   const int64_t unit = fp8 ? 16 : 128;
   if (T < 0 || T > NVFP4_FEW_TOKENS)
     return fail(NVFP4_ERR_SHAPE, "T must be in [0, %d] (got %lld)", NVFP4_FEW_TOKENS, (long long)T);
-  if (H < unit || H % unit || I < unit || I % unit || H >= (int64_t(1) << 20) || I >= (int64_t(1) << 20))
-    return fail(NVFP4_ERR_SHAPE, "H and I must be positive multiples of %lld below 2^20 (got %lld, %lld)",
+  if (H < unit || H % unit || I < unit || I % unit || H >= (int64_t(1) << 19) || I >= (int64_t(1) << 19))
+    return fail(NVFP4_ERR_SHAPE, "H and I must be positive multiples of %lld below 2^19 (got %lld, %lld)",
                 (long long)unit, (long long)H, (long long)I);
   if (2 * I * H >= (int64_t(1) << 31)) return fail(NVFP4_ERR_SHAPE, "an expert's weight (2*I*H) must be below 2^31 elements");
   if (E < 1 || E > 4096) return fail(NVFP4_ERR_SHAPE, "E must be in [1, 4096] (got %d)", E);

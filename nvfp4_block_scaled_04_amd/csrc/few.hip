@@ -4,19 +4,28 @@
 //          token and its tokens t;  c_te = sum of w[t][j] over ids[t][j] == e
 //   down:  out[t][n] = bf16( sum over experts e of W2[e][n] . h_te )
 // Weights FP8 (one scale per 128 x 128) or packed NVFP4 (E4M3 per 16, a global
-// scale an expert, taken into c).  Activations are not quantised: x enters the
-// matrix unit as BF16, h as two BF16 (its rounding and what that leaves, 16 bits
-// in all), the weight codes as BF16, which holds them exactly.  Sums in fp32.
+// scale an expert).  Activations are not quantised: the bytes of each live
+// expert's weights, read once, are the bound.
 //
-// Each live expert's weights are read once; their bytes are the bound.  Tokens
-// are the matrix unit's 16 columns, so up to 16 tokens cost what one costs, and
-// the second product adds its experts up in the accumulators: a column whose
-// token did not choose the expert is fed zeros.
+// FP8 weights enter the matrix unit as BF16 (exact), with x as it is and h as two
+// BF16, its rounding and what that leaves (16 bits in all).  NVFP4 weights enter
+// as FP16, in which a scale is one packed product for two weights (exact; in BF16
+// it would be three times the instructions, and decoding them bounds the kernels):
+// x with its exponents moved so that a token's largest just fits (exact down to
+// 2^-29 of that, below off by 2^-30 of it), h rounded to FP16 (11 bits, an eighth
+// of what the rounding of out to BF16 takes) with a power of two for each 16
+// columns.  Sums in fp32.
 //
-// A workgroup's eight waves split the K blocks of 128 of its tile and join
-// through LDS in wave order (equal inputs give equal bits).  A wave's loads go on
-// across tile ends, kDepth blocks ahead.
-#include <atomic>
+// An expert has few tokens, so the matrix unit's 16 rows are 4 weight rows x 4
+// quarters of a K step, and its 16 columns 4 tokens x the same quarters: of the
+// 16 x 16 results those of equal quarters count (64 of 256; the unit has the
+// room).  Weights so come in runs of 256 bytes a row, and a step's tokens are
+// loaded in the unit's own layout with no lane to spare.  A K step is 256 columns
+// (FP8) or 512 (NVFP4: four stages of the packed layout), 16 bytes of weights a
+// lane and row group.
+//
+// Equal inputs give equal bits: waves and quarters are joined in a fixed order.
+#include <type_traits>
 
 #include "internal.hpp"
 #include "device.hpp"
@@ -27,8 +36,10 @@ namespace {
 
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef float float4v __attribute__((ext_vector_type(4)));
-typedef float float2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kPairs = kFewTokens * 64;               // (token, slot) pairs at most
@@ -48,22 +59,91 @@ __device__ __forceinline__ float uniform_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)p;
 }
 
-// The experts that have a token, in order of their first pair: expert, its
-// tokens as a bit mask, and the row of its first token in h (rows follow the
-// experts and, inside one, the tokens).
+// barrier without a fence: the loads in flight stay there
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------ the work
+//
+// The live experts in order of their first pair, each cut into entries of at
+// most `cap` tokens.  A row of h is one (expert, token); rows follow the entries.
 struct Live {
-  int n;
-  int e[kPairs], mask[kPairs], row[kPairs];
-  int id[kPairs];               // the pairs' experts, -1 for those without one
-  float w[kPairs];              // and weights
+  int n;                        // entries
+  uint16_t e[kPairs];           // an entry's expert
+  uint16_t row[kPairs];         // its first row
+  uint8_t count[kPairs];        // its rows
+  uint8_t tok[kPairs];          // a row's token
+  float coef[kPairs];           // a row's weight
 };
 
 struct LiveScratch {
-  int first[kMaxExperts];       // first pair of an expert, then its place in the list
+  int first[kMaxExperts];       // first pair of an expert, then its place among the experts
   int count[kPairs / 64];
+  int id[kPairs];               // the pairs' experts, -1 for those without one
+  float w[kPairs];              // and weights
+  int mask[kPairs], row[kPairs];   // an expert's tokens and first row
 };
 
-__device__ void build_live(const FewArgs& p, Live& L, LiveScratch& S) {
+// inclusive sum over the wave's lanes
+__device__ __forceinline__ int scan64(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    v += lane >= o ? u : 0;
+  }
+  return v;
+}
+
+// An expert's entries: tokens `mask`, rows from `row` on, first entry `at`.
+__device__ __forceinline__ void put_entries(Live& L, int e, int mask, int row, int at, int cap) {
+  for (int left = __popc(mask); left > 0; left -= cap, row += cap, ++at) {
+    L.e[at] = (uint16_t)e;
+    L.row[at] = (uint16_t)row;
+    L.count[at] = (uint8_t)(left < cap ? left : cap);
+  }
+}
+
+// At most 64 pairs: a lane a pair, every wave for itself up to the writing.
+__device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L) {
+  const int pairs = p.T * p.k, lane = threadIdx.x & 63;
+  int e = lane < pairs ? p.ids[lane] : -1;
+  const float w = lane < pairs ? p.topk_w[lane] : 0.0f;
+  if (e >= p.E) e = -1;
+  const int t = lane / p.k;
+  uint64_t same = 0;                                     // pairs of this pair's expert
+  int mask = 0;                                          // their tokens
+  float coef = 0.0f;                                     // the token's weight for it
+  bool head = e >= 0;                                    // its first pair with it
+  for (int i = 0, ti = 0, j = 0; i < pairs; ++i) {
+    const bool hit = __builtin_amdgcn_readlane(e, i) == e;
+    const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
+    same |= hit ? uint64_t(1) << i : 0;
+    mask |= hit ? 1 << ti : 0;
+    coef += hit && ti == t ? wi : 0.0f;
+    head = head && !(hit && ti == t && i < lane);
+    if (++j == p.k) { j = 0; ++ti; }
+  }
+  const bool first = e >= 0 && (same & ((uint64_t(1) << lane) - 1)) == 0;
+  const int rows = first ? __popc(mask) : 0, entries = (rows + cap - 1) / cap;
+  const int row_end = scan64(rows), entry_end = scan64(entries);
+  const int row = __shfl(row_end - rows, (int)__ffsll((unsigned long long)same) - 1);
+  if (threadIdx.x < 64) {
+    if (first) put_entries(L, e, mask, row, entry_end - entries, cap);
+    if (head) {
+      const int at = row + __popc(mask & ((1 << t) - 1));
+      L.tok[at] = (uint8_t)t;
+      L.coef[at] = coef;
+    }
+    if (lane == 63) L.n = entry_end;
+  }
+  __syncthreads();
+}
+
+__device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
   const int pairs = p.T * p.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr int kPer = kPairs / kThreads;
   int e[kPer];
@@ -75,8 +155,8 @@ __device__ void build_live(const FewArgs& p, Live& L, LiveScratch& S) {
     e[i] = f < pairs ? p.ids[f] : -1;
     if (e[i] < 0 || e[i] >= p.E) e[i] = -1;
     else atomicMin(&S.first[e[i]], f);
-    L.id[f] = e[i];
-    L.w[f] = f < pairs ? p.topk_w[f] : 0.0f;
+    S.id[f] = e[i];
+    S.w[f] = f < pairs ? p.topk_w[f] : 0.0f;
   }
   __syncthreads();
   uint64_t firsts[kPer];
@@ -86,39 +166,57 @@ __device__ void build_live(const FewArgs& p, Live& L, LiveScratch& S) {
     if (lane == 0) S.count[i * kWaves + wave] = __popcll(firsts[i]);
   }
   __syncthreads();
+  int n = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     int at = 0;
     for (int c = 0; c < i * kWaves + wave; ++c) at += S.count[c];
     if (firsts[i] >> lane & 1) {
       at += __popcll(firsts[i] & ((uint64_t(1) << lane) - 1));
-      L.e[at] = e[i];
-      L.mask[at] = 0;
+      S.mask[at] = 0;
       S.first[e[i]] = at;
     }
   }
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int c = 0; c < kPer * kWaves; ++c) n += S.count[c];
-    L.n = n;
-  }
+  for (int c = 0; c < kPer * kWaves; ++c) n += S.count[c];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (e[i] >= 0) atomicOr(&L.mask[S.first[e[i]]], 1 << ((i * kThreads + (int)threadIdx.x) / p.k));
+    if (e[i] >= 0) atomicOr(&S.mask[S.first[e[i]]], 1 << ((i * kThreads + (int)threadIdx.x) / p.k));
   __syncthreads();
   if (wave == 0) {
-    int run = 0;
-    for (int u0 = 0; u0 < L.n; u0 += 64) {
-      const int u = u0 + lane, own = u < L.n ? __popc(L.mask[u]) : 0;
-      int incl = own;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(incl, o);
-        incl += lane >= o ? v : 0;
+    int row = 0, entry = 0;
+    for (int u0 = 0; u0 < n; u0 += 64) {
+      const int u = u0 + lane, rows = u < n ? __popc(S.mask[u]) : 0, entries = (rows + cap - 1) / cap;
+      const int row_end = scan64(rows), entry_end = scan64(entries);
+      if (u < n) {
+        const int first_row = row + row_end - rows, first_entry = entry + entry_end - entries;
+        put_entries(L, 0, S.mask[u], first_row, first_entry, cap);   // the expert is put in below
+        S.row[u] = first_row;
+        S.mask[u] |= first_entry << 16;
       }
-      if (u < L.n) L.row[u] = run + incl - own;
-      run += __shfl(incl, 63);
+      row += __shfl(row_end, 63);
+      entry += __shfl(entry_end, 63);
+    }
+    if (lane == 0) L.n = entry;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (e[i] < 0) continue;
+    const int f = i * kThreads + threadIdx.x, t = f / p.k, u = S.first[e[i]];
+    const int mask = S.mask[u] & 0xFFFF, entry = S.mask[u] >> 16;
+    bool head = true;
+    float sum = 0.0f;
+    for (int j = t * p.k; j < (t + 1) * p.k; ++j) {
+      if (S.id[j] != e[i]) continue;
+      head = head && j >= f;
+      sum += S.w[j];
+    }
+    if (head) {
+      const int at = __popc(mask & ((1 << t) - 1));
+      L.tok[S.row[u] + at] = (uint8_t)t;
+      L.coef[S.row[u] + at] = sum;
+      if (at % cap == 0) L.e[entry + at / cap] = (uint16_t)e[i];
     }
   }
   __syncthreads();
@@ -127,12 +225,12 @@ __device__ void build_live(const FewArgs& p, Live& L, LiveScratch& S) {
 // One operand of a product: the weights of all experts, N rows of K.
 template <bool FP8>
 struct Weights {
+  static constexpr int kCols = FP8 ? 256 : 512;          // a K step
+  static constexpr int kM = FP8 ? 2 : 4;                 // its matrix instructions a row group
   const uint8_t* q;
   const uint8_t* sf;            // FP8: float scales
-  int64_t N;
-  int K, KB;                    // KB: K blocks of 128
+  int K, KB, KS;                // scale blocks or stages of 128, K steps
   int64_t q_bytes, sf_bytes;    // of one expert
-  int NB;                       // FP8: scale blocks along N
 };
 
 template <bool FP8>
@@ -140,261 +238,539 @@ __device__ __forceinline__ Weights<FP8> weights_of(const uint8_t* q, const void*
   Weights<FP8> w;
   w.q = q;
   w.sf = static_cast<const uint8_t*>(sf);
-  w.N = N;
   w.K = (int)K;
   w.KB = (int)((K + 127) / 128);
-  w.NB = (int)((N + 127) / 128);
+  w.KS = (int)((K + w.kCols - 1) / w.kCols);
   const int64_t Np = (N + NVFP4_PACK_ROWS - 1) / NVFP4_PACK_ROWS * NVFP4_PACK_ROWS;
   w.q_bytes = FP8 ? N * K : Np * (K / 2);
-  w.sf_bytes = FP8 ? (int64_t)w.NB * w.KB * 4 : Np * (K / 16);
+  w.sf_bytes = FP8 ? (N + 127) / 128 * w.KB * 4 : Np * (K / 16);
   return w;
 }
 
-// A wave's share of one K block: RF fragments of 16 weight rows and the tokens.
-// Lane (r = lane & 15, g = lane >> 4) holds row or token r and the columns
-//   FP8    16g .. 16g + 15 and 64 + 16g .. 64 + 16g + 15 of the block,
-//   NVFP4  32g .. 32g + 31,
-// eight of them a matrix instruction.
-template <bool FP8, int RF, int HT>
-struct Step {
-  int4v w[RF][FP8 ? 2 : 1];
-  uint32_t s[FP8 ? 1 : RF];     // NVFP4: the lane's two scale bytes
-  float sb[FP8 ? RF : 1];       // FP8: the block's scale, uniform
-  int4v t[HT][4];               // tokens: HT terms (x: 1, h: 2) of 32 columns
-  bool mine;                    // the lane's token has the expert
+// A lane holds, of weight row group f (4 rows), row r & 3 and of quarter r >> 2
+// the 16 bytes g (r = lane & 15, g = lane >> 4); of token group j, token r & 3 and
+// the same columns.
+template <bool FP8, int RF>
+struct StepW {
+  int4v w[RF];
+  int4v s;                      // NVFP4: the scales of two rows of stage q (16 bytes)
+  float sc[2][2];               // FP8, uniform: scales of two row blocks, two K blocks
 };
 
-__device__ __forceinline__ bf16x8 as_bf16(const int4v& v) { return __builtin_bit_cast(bf16x8, v); }
-
-// Eight weights of the lane's 32 as BF16: number m.
+// Where row group f of a tile begins in one expert's weights, in bytes, K step 0.
 template <bool FP8>
-__device__ __forceinline__ bf16x8 decode8(const int4v* w, uint32_t scales, int m) {
-  uint32_t o[4];
-  if constexpr (FP8) {
-    const int lo = w[m >> 1][2 * (m & 1)], hi = w[m >> 1][2 * (m & 1) + 1];
-    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
-  } else {
-    const float s = m < 2 ? __builtin_amdgcn_cvt_f32_fp8(scales, 0) : __builtin_amdgcn_cvt_f32_fp8(scales, 1);
-    const uint32_t c = w[0][m];
-    const float2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-    const float2v d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
-    o[0] = pack_bf16x2(a[0] * s, a[1] * s);      // exact: 2 + 4 bits of significand
-    o[1] = pack_bf16x2(b[0] * s, b[1] * s);
-    o[2] = pack_bf16x2(d[0] * s, d[1] * s);
-    o[3] = pack_bf16x2(f[0] * s, f[1] * s);
-  }
-  return __builtin_bit_cast(bf16x8, int4v{(int)o[0], (int)o[1], (int)o[2], (int)o[3]});
+__device__ __forceinline__ int group_at(const Weights<FP8>& W, int row) {
+  return FP8 ? row * W.K : ((row / NVFP4_PACK_ROWS) * W.KB * NVFP4_PACK_ROWS + row % NVFP4_PACK_ROWS) * 64;
 }
 
-// A token without the expert gets nothing of it, whatever its weights hold
-// (zeros times a NaN or an infinity would be no zeros).
-template <bool FP8, int RF, int HT>
-__device__ __forceinline__ void add_step(float4v (&acc)[RF], const Step<FP8, RF, HT>& x) {
-#pragma unroll
-  for (int f = 0; f < RF; ++f) {
-    float4v d = float4v{0, 0, 0, 0};
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const bf16x8 w = decode8<FP8>(x.w[f], x.s[FP8 ? 0 : f], m);
-#pragma unroll
-      for (int t = 0; t < HT; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16(x.t[t][m]), d, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v = FP8 ? fmaf(d[i], x.sb[f], acc[f][i]) : acc[f][i] + d[i];
-      acc[f][i] = x.mine ? v : acc[f][i];
-    }
-  }
-}
-
-// Loads of weight rows row[f] .. row[f] + 15 of expert e, K block b; none if !on.
-template <bool FP8, int RF, int HT>
-__device__ __forceinline__ void load_weights(const Weights<FP8>& W, int e, const int (&row)[RF], int b, bool on,
-                                             int lane, Step<FP8, RF, HT>& x) {
-  const int r = lane & 15, g = lane >> 4;
+// Loads of K step b of the row groups at `at` of expert e; none if !on.  Past the
+// caches: each is read once.  block (FP8): the two 128-row blocks that the groups
+// lie in; scale_at (NVFP4): this lane's place in the scales of step 0.
+template <bool FP8, int RF>
+__device__ __forceinline__ void load_weights(const Weights<FP8>& W, int e, const int (&at)[RF], const int (&block)[2],
+                                             uint32_t scale_at, int b, bool on, int lane, StepW<FP8, RF>& x) {
+  const int r = lane & 15, g = lane >> 4, q = r >> 2;
   const auto rq = rsrc_of(W.q + e * W.q_bytes, W.q_bytes);
-  const uint32_t off = on ? 0 : kNowhere;
+  const int step = on ? b : 0;
+  uint32_t to;
   if constexpr (FP8) {
-    const int left = W.K - b * 128;
-    const uint32_t lo = 16 * g < left ? off : kNowhere, hi = 64 + 16 * g < left ? off : kNowhere;
-    const uint32_t at = (uint32_t)r * (uint32_t)W.K + 16 * g;
+    const int col = 64 * q + 16 * g;
+    to = ((uint32_t)(r & 3) * (uint32_t)W.K + col) | (on && col < W.K - b * 256 ? 0 : kNowhere);
+    const float* s = reinterpret_cast<const float*>(W.sf + e * W.sf_bytes) + 2 * b;
 #pragma unroll
-    for (int f = 0; f < RF; ++f) {
-      const int so = on ? row[f] * W.K + b * 128 : 0;
-      x.w[f][0] = __builtin_amdgcn_raw_buffer_load_b128(rq, at | lo, so, 2);
-      x.w[f][1] = __builtin_amdgcn_raw_buffer_load_b128(rq, (at + 64) | hi, so, 2);
-      const float* s = reinterpret_cast<const float*>(W.sf + e * W.sf_bytes) + (row[f] / 128) * W.KB + b;
-      x.sb[f] = uniform_load(on ? s : &kNoScale);
+    for (int i = 0; i < 2; ++i) {
+      const float* si = s + block[i] * W.KB;
+      x.sc[i][0] = uniform_load(on ? si : &kNoScale);
+      x.sc[i][1] = uniform_load(on && 2 * b + 1 < W.KB ? si + 1 : &kNoScale);
     }
   } else {
     const auto rs = rsrc_of(W.sf + e * W.sf_bytes, W.sf_bytes);
-#pragma unroll
-    for (int f = 0; f < RF; ++f) {
-      const int at = on ? ((row[f] / NVFP4_PACK_ROWS) * W.KB + b) * NVFP4_PACK_ROWS + row[f] % NVFP4_PACK_ROWS : 0;
-      x.w[f][0] = __builtin_amdgcn_raw_buffer_load_b128(rq, (uint32_t)(64 * r + 16 * g) | off, at * 64, 2);
-      x.s[f] = __builtin_amdgcn_raw_buffer_load_b16(rs, (uint32_t)(8 * r + 2 * g) | off, at * 8, 2);
-    }
+    x.s = __builtin_amdgcn_raw_buffer_load_b128(rs, scale_at | (on && 4 * b + g < W.KB ? 0 : kNowhere), step * (4 * NVFP4_PACK_ROWS * 8), 2);
+    to = (uint32_t)((q * NVFP4_PACK_ROWS + (r & 3)) * 64 + 16 * g) | (on && 4 * b + q < W.KB ? 0 : kNowhere);
   }
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+    x.w[f] = __builtin_amdgcn_raw_buffer_load_b128(rq, to, at[f] + step * (FP8 ? 256 : 4 * NVFP4_PACK_ROWS * 64), 2);
 }
 
-// Loads of 32 columns of a token's row that starts at byte `row` of the resource.
+// The lane's place of load_weights' scales: rows row0 + 2r and the next of the
+// groups' 4 * RF rows, stage g.
+template <int RF>
+__device__ __forceinline__ uint32_t scale_place(int row0, int end, int KB, int lane) {
+  const int r = lane & 15, g = lane >> 4, row = row0 + 2 * r;
+  return r < 2 * RF && row < end ? (uint32_t)(((row / NVFP4_PACK_ROWS) * KB + g) * NVFP4_PACK_ROWS + row % NVFP4_PACK_ROWS) * 8 : kNowhere;
+}
+
+// NVFP4 scales of a step on their way through the wave's LDS, from the lanes that
+// loaded them to those that hold the weights.
+struct Scales {
+  uint16_t v[4][32][4];         // stage, row, two scales each
+};
+
+// Eight weights of the lane's 16 (FP8: as BF16) or 32 (NVFP4: as FP16): number m.
 template <bool FP8>
-__device__ __forceinline__ void load_tokens(__amdgpu_buffer_rsrc_t rt, uint32_t row, int K, int b, bool on, int lane,
-                                            int4v (&t)[4]) {
-  const int g = lane >> 4;
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int col = FP8 ? 16 * g + 8 * (m & 1) + 64 * (m >> 1) : 32 * g + 8 * m;
-    const bool in = on && b * 128 + col < K;
-    t[m] = __builtin_amdgcn_raw_buffer_load_b128(rt, in ? row + 2 * (b * 128 + col) : kNowhere, 0, 0);
+__device__ __forceinline__ int4v decode8(const int4v& w, half2v s, int m) {
+  int4v o;
+  if constexpr (FP8) {
+    const int lo = w[2 * m], hi = w[2 * m + 1];
+    o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+    o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+    o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+    o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  } else {
+    const half2v t = m < 2 ? half2v{s.x, s.x} : half2v{s.y, s.y};
+    const uint32_t c = w[m];
+    o[0] = __builtin_bit_cast(int, (half2v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 0) * t);
+    o[1] = __builtin_bit_cast(int, (half2v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * t);
+    o[2] = __builtin_bit_cast(int, (half2v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * t);
+    o[3] = __builtin_bit_cast(int, (half2v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * t);
   }
+  return o;
 }
 
-// barrier without a fence: the loads in flight stay there
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+template <bool FP8>
+__device__ __forceinline__ float4v mfma(const int4v& w, const int4v& t, const float4v& c) {
+  if constexpr (FP8) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, t), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, w), __builtin_bit_cast(half8v, t), c, 0, 0, 0);
 }
 
-// UP: tile i is 16 columns of h of one live expert (their gate and up rows);
-// !UP: 16 columns of out, over all live experts.
-template <bool FP8, bool UP>
-__global__ __launch_bounds__(kThreads, 2) void few_kernel(FewArgs p) {
-  constexpr int RF = UP ? 2 : 1, HT = UP ? 1 : 2, kDepth = 4, kStride = 16 * RF + 4;
+// largest over the 16 lanes of a row of them
+__device__ __forceinline__ float max16(float m) {
+  m = fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), 0x128, 0xF, 0xF, true)));
+  m = fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), 0x124, 0xF, 0xF, true)));
+  m = fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), 0x122, 0xF, 0xF, true)));
+  return fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), 0x121, 0xF, 0xF, true)));
+}
+
+// Two BF16 -> two FP16 with `less` (both halves) taken off their exponents; what
+// falls below FP16's smallest exponent is as good as zero.
+__device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 mag = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, v & 0x7FFF7FFFu), __builtin_bit_cast(u16x2, less));
+  return (v & 0x80008000u) | (__builtin_bit_cast(uint32_t, mag) << 3);
+}
+
+// ------------------------------------------------------------ up
+//
+// A tile is 16 columns of h of one entry: their 16 gate and 16 up rows.  `split`
+// waves of a workgroup take its K steps in turn and join through LDS; the
+// workgroup works on 8 / split tiles at a time, and a wave's loads run on across
+// tile ends, kDepth steps ahead.
+
+template <bool FP8, int NG, int kDepth>
+__global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int split) {
+  constexpr int RF = 8, kM = Weights<FP8>::kM, kTok = 4 * NG;
   __shared__ Live L;
   __shared__ union {
     LiveScratch build;
-    float red[2][kWaves][16][kStride];
+    float sums[kWaves][4][kTok][4 * RF + 4];
   } S;
-  build_live(p, L, S.build);
+  __shared__ Scales scales[FP8 ? 1 : kWaves];
+  __shared__ uint32_t largest[kFewTokens];               // NVFP4: of a token's |x|, BF16 bits
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n = __builtin_amdgcn_readfirstlane(L.n), stride = gridDim.x;
-  const auto W = UP ? weights_of<FP8>(p.w1_q, p.w1_sf, 2 * p.I, p.H) : weights_of<FP8>(p.w2_q, p.w2_sf, p.H, p.I);
-  const int per = (int)(p.I / 16);                       // UP: tiles of an expert
-  const int tiles = UP ? n * per : (int)(p.H / 16);
-  if ((int)blockIdx.x >= tiles) return;
-  const int blocks = UP ? W.KB : n * W.KB;
-  const int steps = blocks > kWaves ? (blocks + kWaves - 1) / kWaves : 1;
-  const int total = ((tiles - 1 - (int)blockIdx.x) / stride + 1) * steps;
-  const int64_t h_bytes = (int64_t)p.T * p.k * p.I * 2;
-  const auto rx = rsrc_of(UP ? p.x : p.h_hi, UP ? (int64_t)p.T * p.H * 2 : h_bytes);
-  const auto rl = rsrc_of(UP ? nullptr : p.h_lo, UP ? 0 : h_bytes);
-
-  // where the loads are: step s of tile i, K block b of the list's expert u
-  struct {
-    int i, s, u, b, e, mask, first;
-    int row[RF];
-  } at;
-  auto set_expert = [&]() {
-    const int u = at.u < n ? at.u : 0;
-    at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
-    at.mask = __builtin_amdgcn_readfirstlane(L.mask[u]);
-    at.first = __builtin_amdgcn_readfirstlane(L.row[u]);
-  };
-  auto set_tile = [&]() {
-    at.s = 0;
-    if constexpr (UP) {
-      at.u = at.i / per;
-      at.b = wave;
-      const int c = 16 * (at.i - at.u * per);
-      at.row[0] = FP8 ? c : 2 * c;
-      at.row[1] = FP8 ? (int)p.I + c : 2 * c + 16;
-    } else {
-      at.u = wave / W.KB;
-      at.b = wave - at.u * W.KB;
-      at.row[0] = 16 * at.i;
+  if constexpr (!FP8) {
+    for (int t = wave; t < p.T; t += kWaves) {
+      const uint4* x = reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H);
+      uint32_t m = 0;
+      for (int i = lane; i < p.H / 8; i += 64) {
+        const uint4 v = x[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
+      }
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+      if (lane == 0) largest[t] = m;
     }
-    set_expert();
+  }
+  if (p.T * p.k <= 64) build_small(p, kTok, L);
+  else build_large(p, kTok, L, S.build);
+
+  const int subs = kWaves / split, sub = wave / split, part = wave - sub * split;
+  const int I = (int)p.I, per = I / 16, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
+  const int units = (tiles + subs - 1) / subs, stride = gridDim.x;
+  if ((int)blockIdx.x >= units) return;
+  const auto W = weights_of<FP8>(p.w1_q, p.w1_sf, 2 * p.I, p.H);
+  const int steps = (W.KS + split - 1) / split;
+  const int total = ((units - 1 - (int)blockIdx.x) / stride + 1) * steps;
+  const auto rx = rsrc_of(p.x, (int64_t)p.T * p.H * 2);
+
+  struct Step {
+    StepW<FP8, RF> w;
+    int4v t[NG][kM];
   };
-  auto issue = [&](Step<FP8, RF, HT>& x) {
-    const bool on = at.i < tiles && (UP ? at.b < W.KB : at.u < n);
-    load_weights<FP8, RF, HT>(W, at.e, at.row, at.b, on, lane, x);
-    const bool mine = x.mine = on && (at.mask >> r & 1);
-    const int row = UP ? r : at.first + __popc(at.mask & ((1 << r) - 1));
-    const uint32_t byte = (uint32_t)row * (uint32_t)W.K * 2;
-    load_tokens<FP8>(rx, byte, W.K, at.b, mine, lane, x.t[0]);
-    if constexpr (!UP) load_tokens<FP8>(rl, byte, W.K, at.b, mine, lane, x.t[HT - 1]);
+  struct {
+    int i, s, b, e;
+    int w[RF], block[2];        // the row groups' bytes, and (FP8) their 128-row blocks
+    bool on;
+    uint32_t t[NG], sc;         // this lane's tokens' bytes, and place in the scales
+  } at;
+  auto set_tile = [&]() {
+    const int tile = at.i * subs + sub, u = tile < tiles ? tile / per : 0;
+    at.on = tile < tiles;
+    at.s = 0;
+    at.b = part;
+    const int c0 = 16 * (tile - u * per);
+    at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
+    at.sc = scale_place<RF>(2 * c0, 2 * I, W.KB, lane);
+    // NVFP4 rows are interleaved at 8: columns 4f .. 4f + 3 of a tile's gate at 8 * (f / 2) + 4f, up 8 behind
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      at.w[f] = group_at<FP8>(W, FP8 ? c0 + 4 * (f & 3) + (f < 4 ? 0 : I) : 2 * c0 + 16 * ((f & 3) >> 1) + 4 * (f & 1) + (f < 4 ? 0 : 8));
+    at.block[0] = c0 / 128;
+    at.block[1] = (I + c0) / 128;
+    const int row = L.row[u], count = L.count[u];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int c = 4 * j + (r & 3);
+      at.t[j] = c < count ? (uint32_t)L.tok[row + (c < count ? c : 0)] * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
+    }
+  };
+  auto issue = [&](Step& x) {
+    const bool on = at.on && at.b < W.KS;
+    const uint32_t off = on && W.kCols / 4 * (r >> 2) + W.kCols / 16 * g < W.K - at.b * W.kCols ? 0 : kNowhere;
+    const int so = on ? at.b * W.kCols * 2 : 0;
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) x.t[j][m] = __builtin_amdgcn_raw_buffer_load_b128(rx, (at.t[j] + 16 * m) | off, so, 0);
+    load_weights<FP8, RF>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
     asm volatile("" ::: "memory");                       // issued here, not where they are used
+    at.b += split;
     if (++at.s == steps) {
       at.i += stride;
       set_tile();
+    }
+  };
+
+  float4v acc[NG][RF];
+#pragma unroll
+  for (int j = 0; j < NG; ++j)
+#pragma unroll
+    for (int f = 0; f < RF; ++f) acc[j][f] = float4v{0, 0, 0, 0};
+  uint32_t less[NG];            // NVFP4: taken off the exponents of this lane's tokens
+  auto scale_of = [&](int t) {  // the same for token t, as an exponent
+    const int e = (int)(largest[t] >> 7) - 30;
+    return e > 0 ? e : 0;
+  };
+  auto start = [&](int unit) {
+    const int tile = unit * subs + sub, u = tile < tiles ? tile / per : 0, row = L.row[u], count = L.count[u];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int c = 4 * j + (r & 3);
+      if constexpr (!FP8) less[j] = (uint32_t)scale_of(L.tok[row + (c < count ? c : 0)]) * 0x00800080u;
+    }
+  };
+  auto add = [&](Step& x) {
+    float s0, s1;
+    if constexpr (FP8) {
+      s0 = g < 2 ? x.w.sc[0][0] : x.w.sc[0][1];
+      s1 = g < 2 ? x.w.sc[1][0] : x.w.sc[1][1];
     } else {
-      at.b += kWaves;
-      if constexpr (!UP) {
-        if (at.b >= W.KB) {
-          do { at.b -= W.KB; ++at.u; } while (at.b >= W.KB);
-          set_expert();
+      *reinterpret_cast<int4v*>(&scales[wave].v[g][2 * r][0]) = x.w.s;
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x.t[j][m][i] = (int)move_exponents((uint32_t)x.t[j][m][i], less[j]);
+    }
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+      float4v d[NG];
+#pragma unroll
+      for (int j = 0; j < NG; ++j) d[j] = FP8 ? float4v{0, 0, 0, 0} : acc[j][f];
+      half2v s{0, 0};
+      if constexpr (!FP8)
+        s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales[wave].v[r >> 2][16 * ((f & 3) >> 1) + 4 * (f & 1) + (f < 4 ? 0 : 8) + (r & 3)][g], 1.0f, false);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const int4v w = decode8<FP8>(x.w.w[f], s, m);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) d[j] = mfma<FP8>(w, x.t[j][m], d[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][f][i] = fmaf(d[j][i], f < 4 ? s0 : s1, acc[j][f][i]);
+        } else {
+          acc[j][f] = d[j];
         }
       }
     }
   };
-
-  float4v acc[RF];
+  // the unit's sums over its waves and quarters, SwiGLU, and h as two BF16
+  auto finish = [&](int unit) {
+    lds_barrier();                                       // the last unit's sums are read
+    if ((r >> 2) == g) {
 #pragma unroll
-  for (int f = 0; f < RF; ++f) acc[f] = float4v{0, 0, 0, 0};
-  int flip = 0;
-  auto finish = [&](int i) {
-    auto& red = S.red[flip];
-    flip ^= 1;
+      for (int j = 0; j < NG; ++j)
 #pragma unroll
-    for (int f = 0; f < RF; ++f) {
-      *reinterpret_cast<float4v*>(&red[wave][r][16 * f + 4 * g]) = acc[f];
-      acc[f] = float4v{0, 0, 0, 0};
+        for (int f = 0; f < RF; ++f) *reinterpret_cast<float4v*>(&S.sums[wave][g][4 * j + (r & 3)][4 * f]) = acc[j][f];
     }
-    lds_barrier();
-    const int tok = threadIdx.x >> 4, c = threadIdx.x & 15;
-    if constexpr (UP) {
-      const int u = i / per, mask = L.mask[u];
-      if (threadIdx.x < 256 && (mask >> tok & 1)) {
-        const int e = L.e[u], gate = FP8 ? c : 16 * (c >> 3) + (c & 7), up = gate + (FP8 ? 16 : 8);
-        float a = 0.0f, b = 0.0f, coef = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          a += red[w][tok][gate];
-          b += red[w][tok][up];
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int f = 0; f < RF; ++f) acc[j][f] = float4v{0, 0, 0, 0};
+    lds_barrier();
+    // a thread an output: 16 columns of four tokens a wave, as many waves as tiles
+    if (wave >= subs) return;
+    const int c = lane & 15, t = lane >> 4, tile = unit * subs + wave;
+    if (tile >= tiles) return;
+    const int u = tile / per, e = __builtin_amdgcn_readfirstlane(L.e[u]), row = L.row[u], count = L.count[u];
+    const float g1 = FP8 ? 1.0f : uniform_load(p.gs_w1 + e), g2 = FP8 ? 1.0f : uniform_load(p.gs_w2 + e);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int k = 4 * j + t;
+      float a = 0.0f, b = 0.0f;
+      for (int w = wave * split; w < (wave + 1) * split; ++w) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a += S.sums[w][q][k][c];
+          b += S.sums[w][q][k][16 + c];
         }
-        for (int j = 0; j < p.k; ++j) coef += L.id[tok * p.k + j] == e ? L.w[tok * p.k + j] : 0.0f;
-        if constexpr (!FP8) {
-          const float g1 = p.gs_w1[e];
-          a /= g1;
-          b /= g1;
-          coef /= p.gs_w2[e];
-        }
-        const float h = a / (1.0f + expf(-a)) * b * coef;
+      }
+      if (4 * j >= count) continue;                      // uniform
+      const bool in = k < count;
+      const int at_row = row + (in ? k : 0);
+      const int64_t to = (int64_t)at_row * I + 16 * (tile - u * per) + c;
+      if constexpr (FP8) {
+        const float h = a / (1.0f + expf(-a)) * b * L.coef[at_row];
         const uint32_t hi = pack_bf16x2(h, 0.0f);
         const float rest = h - bf16_to_f32(hi & 0xFFFFu);
-        const int64_t at_h = (int64_t)(L.row[u] + __popc(mask & ((1 << tok) - 1))) * p.I + 16 * (i - u * per) + c;
-        p.h_hi[at_h] = (uint16_t)hi;
-        p.h_lo[at_h] = (uint16_t)pack_bf16x2(rest - rest == 0.0f ? rest : 0.0f, 0.0f);
-      }
-    } else {
-      if (tok < p.T) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += red[w][tok][c];
-        p.out[(int64_t)tok * p.H + 16 * i + c] = (uint16_t)pack_bf16x2(v, 0.0f);
+        if (in) {
+          p.h_hi[to] = (uint16_t)hi;
+          p.h_lo[to] = (uint16_t)pack_bf16x2(rest - rest == 0.0f ? rest : 0.0f, 0.0f);   // none of an infinity
+        }
+      } else {
+        // back to x's own exponents; a token that is not finite gives NaN
+        const uint32_t top = largest[L.tok[at_row]];
+        const float back = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, scale_of(L.tok[at_row]) - 112);
+        a = a * back / g1;
+        b = b * back / g1;
+        const float h = a / (1.0f + expf(-a)) * b * L.coef[at_row] / g2;
+        const int ex = __float_as_uint(max16(fabsf(h))) >> 23;
+        const _Float16 v = (_Float16)ldexpf(h, 141 - ex);   // the 16 columns' largest: 2^14 .. 2^15
+        if (in) {
+          p.h_hi[to] = __builtin_bit_cast(uint16_t, v);
+          if (c == 0) reinterpret_cast<uint8_t*>(p.h_lo)[to >> 4] = (uint8_t)ex;
+        }
       }
     }
   };
 
   at.i = blockIdx.x;
   set_tile();
-  lds_barrier();                                         // the list's scratch becomes the sums' place
-  Step<FP8, RF, HT> x[kDepth];
+  Step x[kDepth];
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) issue(x[d]);
-  int i = blockIdx.x, s = 0;
-  for (int q = 0; q < total; q += kDepth) {
+  int unit = blockIdx.x, s = 0;
+  start(unit);
+  for (int q = 0;; q += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      add_step<FP8, RF, HT>(acc, x[d]);
+      if (q + d >= total) return;
+      add(x[d]);
       issue(x[d]);
-      if (++s == steps && i < tiles) {
+      if (++s == steps) {
+        finish(unit);
+        unit += stride;
+        s = 0;
+        if (q + d + 1 < total) start(unit);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ down
+//
+// A tile is 4 * RF columns of out, over all entries: a workgroup's waves take the
+// K steps of all entries in turn.  What a step gives its tokens is added to the
+// wave's own sums in LDS, [quarter][token][column], so a token gets nothing from
+// experts it did not choose, whatever these hold.
+
+template <bool FP8, int RF, int NG, int kDepth>
+__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
+  constexpr int kM = Weights<FP8>::kM, kTok = 4 * NG, kStride = 4 * RF + 4;
+  __shared__ Live L;
+  __shared__ union {
+    LiveScratch build;
+    float sums[kWaves][4][kFewTokens][kStride];
+  } S;
+  __shared__ Scales scales[FP8 ? 1 : kWaves];
+  if (p.T * p.k <= 64) build_small(p, kTok, L);
+  else build_large(p, kTok, L, S.build);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n = __builtin_amdgcn_readfirstlane(L.n), stride = gridDim.x, T = p.T;
+  const int H = (int)p.H, tiles = (H + 4 * RF - 1) / (4 * RF);
+  const auto W = weights_of<FP8>(p.w2_q, p.w2_sf, p.H, p.I);
+  const int steps = (n * W.KS + kWaves - 1) / kWaves;
+  const int64_t plane = (int64_t)T * p.k * p.I * 2;
+  const auto rh = rsrc_of(p.h_hi, plane), rl = rsrc_of(p.h_lo, FP8 ? plane : plane / 32);
+
+  struct Step {
+    StepW<FP8, RF> w;
+    int4v t[NG][FP8 ? 2 : 1][kM];
+    uint64_t ex[FP8 ? 1 : NG];  // NVFP4: the exponents of the lane's quarter's 8 x 16 columns
+    int tok[NG];                // the token of this lane's results, or -1
+    int cut;                    // FP8: row groups in the tile's first row block
+  };
+  struct {
+    int i, s, u, b, e;
+    int w[RF], block[2], cut;
+    uint32_t t[NG], ex[NG], sc;
+    int tok[NG];
+  } at;
+  auto set_entry = [&]() {
+    const int u = at.u < n ? at.u : 0;
+    at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
+    const int row = L.row[u], count = at.u < n ? L.count[u] : 0;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int c = 4 * j + (r & 3);
+      at.t[j] = c < count ? (uint32_t)(row + c) * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
+      at.ex[j] = c < count ? (uint32_t)(row + c) * (uint32_t)(W.K / 16) + 8 * (r >> 2) : kNowhere;
+      at.tok[j] = c < count && (r >> 2) == g ? L.tok[row + (c < count ? c : 0)] : -1;
+    }
+  };
+  auto set_tile = [&]() {
+    at.s = 0;
+    at.u = wave / W.KS;
+    at.b = wave - at.u * W.KS;
+    const int row0 = 4 * RF * at.i;
+    at.sc = scale_place<RF>(row0, H, W.KB, lane);
+#pragma unroll
+    for (int f = 0; f < RF; ++f) at.w[f] = group_at<FP8>(W, row0 + 4 * f < H ? row0 + 4 * f : H - 4);   // none behind the last row
+    at.block[0] = (row0 < H ? row0 : H - 4) / 128;
+    at.block[1] = (row0 + 4 * RF < H ? row0 + 4 * RF - 4 : H - 4) / 128;
+    at.cut = (at.block[0] + 1) * 32 - row0 / 4;
+    set_entry();
+  };
+  auto issue = [&](Step& x) {
+    const bool on = at.i < tiles && at.u < n;
+    const uint32_t off = on && W.kCols / 4 * (r >> 2) + W.kCols / 16 * g < W.K - at.b * W.kCols ? 0 : kNowhere;
+    const int so = on ? at.b * W.kCols * 2 : 0;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        x.t[j][0][m] = __builtin_amdgcn_raw_buffer_load_b128(rh, (at.t[j] + 16 * m) | off, so, 0);
+        if constexpr (FP8) x.t[j][FP8 ? 1 : 0][m] = __builtin_amdgcn_raw_buffer_load_b128(rl, (at.t[j] + 16 * m) | off, so, 0);
+      }
+      if constexpr (!FP8) x.ex[j] = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rl, at.ex[j] | off, on ? at.b * 32 : 0, 0));
+      x.tok[j] = at.tok[j];
+    }
+    load_weights<FP8, RF>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
+    x.cut = at.cut;
+    asm volatile("" ::: "memory");                       // issued here, not where they are used
+    if (++at.s == steps) {
+      at.i += stride;
+      set_tile();
+    } else {
+      at.b += kWaves;
+      if (at.b >= W.KS) {
+        do { at.b -= W.KS; ++at.u; } while (at.b >= W.KS);
+        set_entry();
+      }
+    }
+  };
+  auto add = [&](Step& x) {
+    float s0, s1, back[NG];
+    if constexpr (FP8) {
+      s0 = g < 2 ? x.w.sc[0][0] : x.w.sc[0][1];
+      s1 = g < 2 ? x.w.sc[1][0] : x.w.sc[1][1];
+    } else {
+      *reinterpret_cast<int4v*>(&scales[wave].v[g][2 * r][0]) = x.w.s;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        // this quarter's columns to one power of two: its largest
+        int top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, (int)(x.ex[j] >> (8 * i) & 255));
+        const uint32_t own = (uint32_t)(x.ex[j] >> (16 * g));
+        const half2v f0 = half2v{1, 1} * (_Float16)ldexpf(1.0f, (int)(own & 255) - top), f1 = half2v{1, 1} * (_Float16)ldexpf(1.0f, (int)(own >> 8 & 255) - top);
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int two = x.t[j][0][m][i];
+            x.t[j][0][m][i] = __builtin_bit_cast(int, __builtin_bit_cast(half2v, two) * (m < 2 ? f0 : f1));
+          }
+        back[j] = ldexpf(1.0f, top - 141);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+      float4v d[NG];
+#pragma unroll
+      for (int j = 0; j < NG; ++j) d[j] = float4v{0, 0, 0, 0};
+      half2v s{0, 0};
+      if constexpr (!FP8) s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales[wave].v[r >> 2][4 * f + (r & 3)][g], 1.0f, false);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const int4v w = decode8<FP8>(x.w.w[f], s, m);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          d[j] = mfma<FP8>(w, x.t[j][0][m], d[j]);
+          if constexpr (FP8) d[j] = mfma<FP8>(w, x.t[j][FP8 ? 1 : 0][m], d[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if (x.tok[j] < 0) continue;
+        const float sc = !FP8 ? back[j] : f < x.cut ? s0 : s1;
+        float4v* to = reinterpret_cast<float4v*>(&S.sums[wave][g][x.tok[j]][4 * f]);
+        float4v v = *to;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(d[j][i], sc, v[i]);
+        *to = v;
+      }
+    }
+  };
+  auto clear = [&]() {
+    float4v* own = reinterpret_cast<float4v*>(&S.sums[wave][0][0][0]);
+    for (int i = lane; i < 4 * kFewTokens * kStride / 4; i += 64) own[i] = float4v{0, 0, 0, 0};
+  };
+  // the tile's sums over waves and quarters, and out
+  auto finish = [&](int i) {
+    lds_barrier();
+    const int q = threadIdx.x & 3;
+    for (int o = threadIdx.x >> 2; o < T * 4 * RF; o += kThreads / 4) {
+      const int t = o / (4 * RF), c = o - t * (4 * RF);
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v += S.sums[w][q][t][c];
+      v += __shfl_xor(v, 1);
+      v += __shfl_xor(v, 2);
+      if (q == 0 && 4 * RF * i + c < H) p.out[(int64_t)t * H + 4 * RF * i + c] = (uint16_t)pack_bf16x2(v, 0.0f);
+    }
+    lds_barrier();
+    clear();
+  };
+
+  at.i = blockIdx.x;
+  set_tile();
+  Step x[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) issue(x[d]);
+  clear();
+  if (steps == 0) {                                      // no token has an expert
+    for (int i = blockIdx.x; i < tiles; i += stride) finish(i);
+    return;
+  }
+  const int total = ((tiles - 1 - (int)blockIdx.x) / stride + 1) * steps;
+  int i = blockIdx.x, s = 0;
+  for (int q = 0;; q += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (q + d >= total) return;
+      add(x[d]);
+      issue(x[d]);
+      if (++s == steps) {
         finish(i);
         i += stride;
         s = 0;
@@ -403,13 +779,31 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(FewArgs p) {
   }
 }
 
-template <bool FP8>
+template <bool FP8, int NG>
 hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
-  const int64_t pairs = (int64_t)a.T * a.k, live = pairs < a.E ? pairs : a.E, up = live * (a.I / 16), down = a.H / 16;
-  few_kernel<FP8, true><<<(unsigned)(up < cus ? up : cus), kThreads, 0, stream>>>(a);
+  const int64_t pairs = (int64_t)a.T * a.k, live = pairs < a.E ? pairs : a.E;
+  // waves a tile of the first product: as many as give the fewest rounds of K steps
+  const int64_t tiles = live * (a.I / 16), ks = (a.H + Weights<FP8>::kCols - 1) / Weights<FP8>::kCols;
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  int split = kWaves;
+  int64_t best = up(tiles, cus) * up(ks, kWaves);
+  for (int s = kWaves / 2; s >= 1; s /= 2) {
+    const int64_t c = up(up(tiles * s, kWaves), cus) * up(ks, s);
+    if (c < best) { best = c; split = s; }
+  }
+  const int64_t units = up(tiles * split, kWaves);
+  few_up_kernel<FP8, NG, NG == 1 ? 3 : 2><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(a, split);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  few_kernel<FP8, false><<<(unsigned)(down < 2 * cus ? down : 2 * cus), kThreads, 0, stream>>>(a);
+  auto down = [&](auto rf) {
+    constexpr int RF = decltype(rf)::value;
+    const int64_t t = up(a.H, 4 * RF);
+    few_down_kernel<FP8, RF, NG, NG == 1 ? 3 : 2><<<(unsigned)(t < cus ? t : cus), kThreads, 0, stream>>>(a);
+  };
+  if (a.H <= 8 * cus) down(std::integral_constant<int, 2>{});
+  else if (a.H <= 16 * cus) down(std::integral_constant<int, 4>{});
+  else if (a.H <= 28 * cus) down(std::integral_constant<int, 7>{});
+  else down(std::integral_constant<int, 8>{});
   return hipGetLastError();
 }
 
@@ -419,7 +813,9 @@ hipError_t launch_few(const FewArgs& a, hipStream_t stream) {
   int cus = 0;
   const hipError_t err = device_cus(cus);
   if (err != hipSuccess) return err;
-  return a.fp8 ? launch<true>(a, cus, stream) : launch<false>(a, cus, stream);
+  const bool busy = a.T > 4 && (int64_t)a.T * a.k > 2 * (int64_t)a.E;
+  if (a.fp8) return busy ? launch<true, 2>(a, cus, stream) : launch<true, 1>(a, cus, stream);
+  return busy ? launch<false, 2>(a, cus, stream) : launch<false, 1>(a, cus, stream);
 }
 
 }  // namespace nvfp4

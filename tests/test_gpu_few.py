@@ -62,7 +62,8 @@ def _routing(rng, T, E, k, bad=0.0, few=None):
 
 
 def _check(out, x, ids, w, w1, w2):
-    ref, err = W.forward(x.float().numpy(), ids, w, w1, w2)
+    # h: 11 bits at least (half a step is 2^-12 of it)
+    ref, err = W.forward(x.float().numpy(), ids, w, w1, w2, h_bits=12)
     got = bf16_values(host(out))
     worst = np.max(np.abs(got - ref) / err)
     print(f"[worst share of the bound] {worst:.3f}", flush=True)
