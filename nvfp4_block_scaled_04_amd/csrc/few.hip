@@ -107,32 +107,48 @@ __device__ __forceinline__ void put_entries(Live& L, int e, int mask, int row, i
   }
 }
 
-// At most 64 pairs: a lane a pair, every wave for itself up to the writing.
-__device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L) {
-  const int pairs = p.T * p.k, lane = threadIdx.x & 63;
-  int e = lane < pairs ? p.ids[lane] : -1;
-  const float w = lane < pairs ? p.topk_w[lane] : 0.0f;
-  if (e >= p.E) e = -1;
-  const int t = lane / p.k;
-  uint64_t same = 0;                                     // pairs of this pair's expert
-  int mask = 0;                                          // their tokens
-  float coef = 0.0f;                                     // the token's weight for it
-  bool head = e >= 0;                                    // its first pair with it
-  for (int i = 0, ti = 0, j = 0; i < pairs; ++i) {
-    const bool hit = __builtin_amdgcn_readlane(e, i) == e;
-    const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
-    same |= hit ? uint64_t(1) << i : 0;
-    mask |= hit ? 1 << ti : 0;
-    coef += hit && ti == t ? wi : 0.0f;
-    head = head && !(hit && ti == t && i < lane);
-    if (++j == p.k) { j = 0; ++ti; }
-  }
-  const bool first = e >= 0 && (same & ((uint64_t(1) << lane) - 1)) == 0;
-  const int rows = first ? __popc(mask) : 0, entries = (rows + cap - 1) / cap;
-  const int row_end = scan64(rows), entry_end = scan64(entries);
-  const int row = __shfl(row_end - rows, (int)__ffsll((unsigned long long)same) - 1);
+// At most 64 pairs: one wave, a lane a pair.  Pairs of one expert find each other
+// by writing their lane to the expert's place: whichever stays there collects for
+// all of them.
+__device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
   if (threadIdx.x < 64) {
-    if (first) put_entries(L, e, mask, row, entry_end - entries, cap);
+    const int pairs = p.T * p.k, lane = threadIdx.x;
+    const int e = lane < pairs ? p.ids[lane] : -1, t = lane / p.k;
+    const float w = lane < pairs ? p.topk_w[lane] : 0.0f;
+    const bool on = e >= 0 && e < p.E;
+    int *mask_of = S.mask, *first_of = S.row, *count_of = S.id;
+    mask_of[lane] = 0;
+    first_of[lane] = 64;
+    count_of[lane] = 0;
+    if (on) S.first[e] = lane;
+    __builtin_amdgcn_wave_barrier();
+    int mask = 0, first = 64, count = 0, by = 0;
+    if (on) {
+      by = S.first[e];
+      atomicOr(&mask_of[by], 1 << t);
+      atomicMin(&first_of[by], lane);
+      atomicAdd(&count_of[by], 1);
+      __builtin_amdgcn_wave_barrier();
+      mask = mask_of[by];
+      first = first_of[by];
+      count = count_of[by];
+    }
+    const int tokens = __popc(mask), rows = first == lane ? tokens : 0, entries = (rows + cap - 1) / cap;
+    const int row_end = scan64(rows), entry_end = scan64(entries);
+    const int row = __shfl(row_end - rows, first & 63);
+    bool head = on;                                      // the token's first pair with the expert
+    float coef = w;                                      // and all its pairs' weights
+    if (__ballot(count != tokens) != 0) {                // an expert twice in a token's row
+      coef = 0.0f;
+      for (int j = 0; j < p.k; ++j) {
+        const int f = t * p.k + j;
+        const bool hit = __shfl(e, f & 63) == e && f < pairs;
+        const float wj = __shfl(w, f & 63);
+        coef += hit ? wj : 0.0f;
+        head = head && !(hit && f < lane);
+      }
+    }
+    if (rows) put_entries(L, e, mask, row, entry_end - entries, cap);
     if (head) {
       const int at = row + __popc(mask & ((1 << t) - 1));
       L.tok[at] = (uint8_t)t;
@@ -143,9 +159,10 @@ __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L) 
   __syncthreads();
 }
 
+template <int kWaves>
 __device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
   const int pairs = p.T * p.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kPer = kPairs / kThreads;
+  constexpr int kThreads = kWaves * 64, kPer = kPairs / kThreads;
   int e[kPer];
   for (int i = threadIdx.x; i < p.E; i += kThreads) S.first[i] = 0x7FFFFFFF;
   __syncthreads();
@@ -265,8 +282,11 @@ __device__ __forceinline__ int group_at(const Weights<FP8>& W, int row) {
 
 // Loads of K step b of the row groups at `at` of expert e; none if !on.  Past the
 // caches: each is read once.  block (FP8): the two 128-row blocks that the groups
-// lie in; scale_at (NVFP4): this lane's place in the scales of step 0.
-template <bool FP8, int RF>
+// lie in; scale_at (NVFP4): this lane's place in the scales of step 0.  TURN: the
+// groups are eight in a row, 256 bytes each, and load f takes group f ^ q of
+// quarter q: stages are 32 KiB apart, so one group's quarters would all come from
+// one memory channel (sixteen tokens, first product: 327 us, turned 308).
+template <bool FP8, int RF, bool TURN>
 __device__ __forceinline__ void load_weights(const Weights<FP8>& W, int e, const int (&at)[RF], const int (&block)[2],
                                              uint32_t scale_at, int b, bool on, int lane, StepW<FP8, RF>& x) {
   const int r = lane & 15, g = lane >> 4, q = r >> 2;
@@ -289,8 +309,10 @@ __device__ __forceinline__ void load_weights(const Weights<FP8>& W, int e, const
     to = (uint32_t)((q * NVFP4_PACK_ROWS + (r & 3)) * 64 + 16 * g) | (on && 4 * b + q < W.KB ? 0 : kNowhere);
   }
 #pragma unroll
-  for (int f = 0; f < RF; ++f)
-    x.w[f] = __builtin_amdgcn_raw_buffer_load_b128(rq, to, at[f] + step * (FP8 ? 256 : 4 * NVFP4_PACK_ROWS * 64), 2);
+  for (int f = 0; f < RF; ++f) {
+    const int so = at[TURN ? 0 : f] + step * (FP8 ? 256 : 4 * NVFP4_PACK_ROWS * 64);
+    x.w[f] = __builtin_amdgcn_raw_buffer_load_b128(rq, TURN ? to + 256 * (f ^ q) : to, so, 2);
+  }
 }
 
 // The lane's place of load_weights' scales: rows row0 + 2r and the next of the
@@ -384,8 +406,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
       if (lane == 0) largest[t] = m;
     }
   }
-  if (p.T * p.k <= 64) build_small(p, kTok, L);
-  else build_large(p, kTok, L, S.build);
+  if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
+  else build_large<kWaves>(p, kTok, L, S.build);
 
   const int subs = kWaves / split, sub = wave / split, part = wave - sub * split;
   const int I = (int)p.I, per = I / 16, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
@@ -414,10 +436,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     const int c0 = 16 * (tile - u * per);
     at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
     at.sc = scale_place<RF>(2 * c0, 2 * I, W.KB, lane);
-    // NVFP4 rows are interleaved at 8: columns 4f .. 4f + 3 of a tile's gate at 8 * (f / 2) + 4f, up 8 behind
+    // FP8: four groups of gate rows, then of up rows; NVFP4: 32 rows, eight of each in turn
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
-      at.w[f] = group_at<FP8>(W, FP8 ? c0 + 4 * (f & 3) + (f < 4 ? 0 : I) : 2 * c0 + 16 * ((f & 3) >> 1) + 4 * (f & 1) + (f < 4 ? 0 : 8));
+    for (int f = 0; f < RF; ++f) at.w[f] = group_at<FP8>(W, FP8 ? c0 + 4 * (f & 3) + (f < 4 ? 0 : I) : 2 * c0 + 4 * f);
     at.block[0] = c0 / 128;
     at.block[1] = (I + c0) / 128;
     const int row = L.row[u], count = L.count[u];
@@ -435,7 +456,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int m = 0; m < kM; ++m) x.t[j][m] = __builtin_amdgcn_raw_buffer_load_b128(rx, (at.t[j] + 16 * m) | off, so, 0);
-    load_weights<FP8, RF>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
+    load_weights<FP8, RF, !FP8>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
     asm volatile("" ::: "memory");                       // issued here, not where they are used
     at.b += split;
     if (++at.s == steps) {
@@ -454,7 +475,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     const int e = (int)(largest[t] >> 7) - 30;
     return e > 0 ? e : 0;
   };
+  float g1 = 1.0f, g2 = 1.0f;   // NVFP4: the global scales of the tile that this wave finishes
   auto start = [&](int unit) {
+    if constexpr (!FP8) {
+      const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.e[wave < subs && mine < tiles ? mine / per : 0]);
+      g1 = uniform_load(p.gs_w1 + e);
+      g2 = uniform_load(p.gs_w2 + e);
+    }
     const int tile = unit * subs + sub, u = tile < tiles ? tile / per : 0, row = L.row[u], count = L.count[u];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
@@ -483,7 +510,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
       for (int j = 0; j < NG; ++j) d[j] = FP8 ? float4v{0, 0, 0, 0} : acc[j][f];
       half2v s{0, 0};
       if constexpr (!FP8)
-        s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales[wave].v[r >> 2][16 * ((f & 3) >> 1) + 4 * (f & 1) + (f < 4 ? 0 : 8) + (r & 3)][g], 1.0f, false);
+        s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales[wave].v[r >> 2][4 * (f ^ (r >> 2)) + (r & 3)][g], 1.0f, false);
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int4v w = decode8<FP8>(x.w.w[f], s, m);
@@ -503,24 +530,25 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
   };
   // the unit's sums over its waves and quarters, SwiGLU, and h as two BF16
   auto finish = [&](int unit) {
-    lds_barrier();                                       // the last unit's sums are read
+    if (split > 1) lds_barrier();                        // the last unit's sums are read
     if ((r >> 2) == g) {
 #pragma unroll
       for (int j = 0; j < NG; ++j)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) *reinterpret_cast<float4v*>(&S.sums[wave][g][4 * j + (r & 3)][4 * f]) = acc[j][f];
+        for (int f = 0; f < RF; ++f) *reinterpret_cast<float4v*>(&S.sums[wave][g][4 * j + (r & 3)][FP8 ? 4 * f : 4 * (f ^ g)]) = acc[j][f];
     }
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int f = 0; f < RF; ++f) acc[j][f] = float4v{0, 0, 0, 0};
-    lds_barrier();
+    if (split > 1) lds_barrier();
+    else __builtin_amdgcn_wave_barrier();
     // a thread an output: 16 columns of four tokens a wave, as many waves as tiles
     if (wave >= subs) return;
     const int c = lane & 15, t = lane >> 4, tile = unit * subs + wave;
+    const int gate = FP8 ? c : 16 * (c >> 3) + (c & 7), up = gate + (FP8 ? 16 : 8);
     if (tile >= tiles) return;
-    const int u = tile / per, e = __builtin_amdgcn_readfirstlane(L.e[u]), row = L.row[u], count = L.count[u];
-    const float g1 = FP8 ? 1.0f : uniform_load(p.gs_w1 + e), g2 = FP8 ? 1.0f : uniform_load(p.gs_w2 + e);
+    const int u = tile / per, row = L.row[u], count = L.count[u];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int k = 4 * j + t;
@@ -528,8 +556,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
       for (int w = wave * split; w < (wave + 1) * split; ++w) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          a += S.sums[w][q][k][c];
-          b += S.sums[w][q][k][16 + c];
+          a += S.sums[w][q][k][gate];
+          b += S.sums[w][q][k][up];
         }
       }
       if (4 * j >= count) continue;                      // uniform
@@ -591,8 +619,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
 // wave's own sums in LDS, [quarter][token][column], so a token gets nothing from
 // experts it did not choose, whatever these hold.
 
-template <bool FP8, int RF, int NG, int kDepth>
-__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
+template <bool FP8, int RF, int NG, int kDepth, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewArgs p) {
   constexpr int kM = Weights<FP8>::kM, kTok = 4 * NG, kStride = 4 * RF + 4;
   __shared__ Live L;
   __shared__ union {
@@ -600,8 +628,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
     float sums[kWaves][4][kFewTokens][kStride];
   } S;
   __shared__ Scales scales[FP8 ? 1 : kWaves];
-  if (p.T * p.k <= 64) build_small(p, kTok, L);
-  else build_large(p, kTok, L, S.build);
+  if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
+  else build_large<kWaves>(p, kTok, L, S.build);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -664,7 +692,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
       if constexpr (!FP8) x.ex[j] = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rl, at.ex[j] | off, on ? at.b * 32 : 0, 0));
       x.tok[j] = at.tok[j];
     }
-    load_weights<FP8, RF>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
+    load_weights<FP8, RF, false>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
     x.cut = at.cut;
     asm volatile("" ::: "memory");                       // issued here, not where they are used
     if (++at.s == steps) {
@@ -739,7 +767,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
   auto finish = [&](int i) {
     lds_barrier();
     const int q = threadIdx.x & 3;
-    for (int o = threadIdx.x >> 2; o < T * 4 * RF; o += kThreads / 4) {
+    for (int o = threadIdx.x >> 2; o < T * 4 * RF; o += kWaves * 16) {
       const int t = o / (4 * RF), c = o - t * (4 * RF);
       float v = 0.0f;
 #pragma unroll
@@ -782,23 +810,25 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
 template <bool FP8, int NG>
 hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
   const int64_t pairs = (int64_t)a.T * a.k, live = pairs < a.E ? pairs : a.E;
-  // waves a tile of the first product: as many as give the fewest rounds of K steps
+  // Waves a tile of the first product: the fewest rounds of its K steps, the join
+  // of several waves counted as two steps, a wave's own end of a tile as one.
   const int64_t tiles = live * (a.I / 16), ks = (a.H + Weights<FP8>::kCols - 1) / Weights<FP8>::kCols;
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   int split = kWaves;
-  int64_t best = up(tiles, cus) * up(ks, kWaves);
-  for (int s = kWaves / 2; s >= 1; s /= 2) {
-    const int64_t c = up(up(tiles * s, kWaves), cus) * up(ks, s);
+  int64_t best = INT64_MAX;
+  for (int s = kWaves; s >= 1; s /= 2) {
+    const int64_t c = up(up(tiles * s, kWaves), cus) * (up(ks, s) + (s > 1 ? 2 : 1));
     if (c < best) { best = c; split = s; }
   }
   const int64_t units = up(tiles * split, kWaves);
-  few_up_kernel<FP8, NG, NG == 1 ? 3 : 2><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(a, split);
+  few_up_kernel<FP8, NG, 2><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(a, split);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   auto down = [&](auto rf) {
     constexpr int RF = decltype(rf)::value;
     const int64_t t = up(a.H, 4 * RF);
-    few_down_kernel<FP8, RF, NG, NG == 1 ? 3 : 2><<<(unsigned)(t < cus ? t : cus), kThreads, 0, stream>>>(a);
+    constexpr int waves = RF <= 4 && NG == 1 ? 16 : 8;
+    few_down_kernel<FP8, RF, NG, 2, waves><<<(unsigned)(t < cus ? t : cus), waves * 64, 0, stream>>>(a);
   };
   if (a.H <= 8 * cus) down(std::integral_constant<int, 2>{});
   else if (a.H <= 16 * cus) down(std::integral_constant<int, 4>{});

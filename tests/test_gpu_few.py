@@ -74,6 +74,9 @@ CASES = [("fp8", 1, 16, 16, 1, 1, 0.0, None), ("fp8", 1, 128, 128, 4, 2, 0.0, No
          ("fp8", 16, 1040, 528, 40, 3, 0.1, None), ("fp8", 16, 256, 128, 9, 2, 0.0, 2), ("fp8", 13, 2048, 768, 20, 8, 0.0, None),
          ("fp8", 4, 1152, 16, 3, 2, 0.0, None), ("fp8", 16, 64, 32, 300, 64, 0.2, None), ("fp8", 2, 16, 1040, 4, 4, 0.0, None),
          ("fp8", 1, 7168, 2048, 6, 8, 0.0, None), ("fp8", 7, 32, 32, 4096, 5, 0.0, None),
+         ("fp8", 3, 4096, 64, 3, 2, 0.0, None), ("fp8", 16, 8256, 48, 5, 2, 0.0, None), ("fp8", 2, 20496, 32, 2, 2, 0.0, None),
+         ("fp8", 12, 3088, 80, 2, 2, 0.0, None), ("nvfp4", 3, 4096, 128, 3, 2, 0.0, None), ("nvfp4", 16, 8448, 128, 4, 3, 0.0, None),
+         ("nvfp4", 2, 20480, 128, 2, 2, 0.0, None), ("nvfp4", 12, 2816, 256, 2, 2, 0.0, None), ("nvfp4", 4, 256, 640, 40, 16, 0.1, None),
          ("nvfp4", 1, 128, 128, 1, 1, 0.0, None), ("nvfp4", 16, 256, 128, 4, 2, 0.0, None), ("nvfp4", 7, 384, 256, 9, 3, 0.2, None),
          ("nvfp4", 2, 640, 1152, 3, 2, 0.0, None), ("nvfp4", 16, 512, 384, 30, 8, 0.0, 3), ("nvfp4", 1, 7168, 2048, 6, 8, 0.0, None),
          ("nvfp4", 5, 1152, 640, 12, 64, 0.5, None), ("nvfp4", 3, 1024, 896, 17, 4, 0.0, None)]
