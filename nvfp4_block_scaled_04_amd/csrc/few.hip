@@ -70,12 +70,15 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // The live experts in order of their first pair, each cut into entries of at
 // most `cap` tokens.  A row of h is one (expert, token); rows follow the entries.
+struct Entry {
+  uint16_t e, row;              // expert, first row
+  uint32_t count;               // rows
+  uint8_t tok[8];               // their tokens
+};
+
 struct Live {
   int n;                        // entries
-  uint16_t e[kPairs];           // an entry's expert
-  uint16_t row[kPairs];         // its first row
-  uint8_t count[kPairs];        // its rows
-  uint8_t tok[kPairs];          // a row's token
+  Entry entry[kPairs];
   float coef[kPairs];           // a row's weight
 };
 
@@ -98,12 +101,13 @@ __device__ __forceinline__ int scan64(int v) {
   return v;
 }
 
-// An expert's entries: tokens `mask`, rows from `row` on, first entry `at`.
-__device__ __forceinline__ void put_entries(Live& L, int e, int mask, int row, int at, int cap) {
-  for (int left = __popc(mask); left > 0; left -= cap, row += cap, ++at) {
-    L.e[at] = (uint16_t)e;
-    L.row[at] = (uint16_t)row;
-    L.count[at] = (uint8_t)(left < cap ? left : cap);
+// An expert's entries: `rows` rows from `row` on, first entry `at`; their tokens
+// and weights come from the pairs.
+__device__ __forceinline__ void put_entries(Live& L, int e, int rows, int row, int at, int cap) {
+  for (; rows > 0; rows -= cap, row += cap, ++at) {
+    L.entry[at].e = (uint16_t)e;
+    L.entry[at].row = (uint16_t)row;
+    L.entry[at].count = (uint32_t)(rows < cap ? rows : cap);
   }
 }
 
@@ -135,7 +139,7 @@ __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, 
     }
     const int tokens = __popc(mask), rows = first == lane ? tokens : 0, entries = (rows + cap - 1) / cap;
     const int row_end = scan64(rows), entry_end = scan64(entries);
-    const int row = __shfl(row_end - rows, first & 63);
+    const int row = __shfl(row_end - rows, first & 63), entry = __shfl(entry_end - entries, first & 63);
     bool head = on;                                      // the token's first pair with the expert
     float coef = w;                                      // and all its pairs' weights
     if (__ballot(count != tokens) != 0) {                // an expert twice in a token's row
@@ -148,21 +152,20 @@ __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, 
         head = head && !(hit && f < lane);
       }
     }
-    if (rows) put_entries(L, e, mask, row, entry_end - entries, cap);
+    put_entries(L, e, rows, row, entry, cap);
     if (head) {
-      const int at = row + __popc(mask & ((1 << t) - 1));
-      L.tok[at] = (uint8_t)t;
-      L.coef[at] = coef;
+      const int at = __popc(mask & ((1 << t) - 1));
+      L.entry[entry + at / cap].tok[at % cap] = (uint8_t)t;
+      L.coef[row + at] = coef;
     }
     if (lane == 63) L.n = entry_end;
   }
   __syncthreads();
 }
 
-template <int kWaves>
 __device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
   const int pairs = p.T * p.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kThreads = kWaves * 64, kPer = kPairs / kThreads;
+  constexpr int kPer = kPairs / kThreads;
   int e[kPer];
   for (int i = threadIdx.x; i < p.E; i += kThreads) S.first[i] = 0x7FFFFFFF;
   __syncthreads();
@@ -207,7 +210,7 @@ __device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) 
       const int row_end = scan64(rows), entry_end = scan64(entries);
       if (u < n) {
         const int first_row = row + row_end - rows, first_entry = entry + entry_end - entries;
-        put_entries(L, 0, S.mask[u], first_row, first_entry, cap);   // the expert is put in below
+        put_entries(L, 0, rows, first_row, first_entry, cap);   // the expert is put in below
         S.row[u] = first_row;
         S.mask[u] |= first_entry << 16;
       }
@@ -231,9 +234,9 @@ __device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) 
     }
     if (head) {
       const int at = __popc(mask & ((1 << t) - 1));
-      L.tok[S.row[u] + at] = (uint8_t)t;
+      L.entry[entry + at / cap].tok[at % cap] = (uint8_t)t;
       L.coef[S.row[u] + at] = sum;
-      if (at % cap == 0) L.e[entry + at / cap] = (uint16_t)e[i];
+      if (at % cap == 0) L.entry[entry + at / cap].e = (uint16_t)e[i];
     }
   }
   __syncthreads();
@@ -407,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     }
   }
   if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
-  else build_large<kWaves>(p, kTok, L, S.build);
+  else build_large(p, kTok, L, S.build);
 
   const int subs = kWaves / split, sub = wave / split, part = wave - sub * split;
   const int I = (int)p.I, per = I / 16, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
@@ -434,18 +437,18 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     at.s = 0;
     at.b = part;
     const int c0 = 16 * (tile - u * per);
-    at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
+    const Entry& y = L.entry[u];
+    at.e = __builtin_amdgcn_readfirstlane(y.e);
     at.sc = scale_place<RF>(2 * c0, 2 * I, W.KB, lane);
     // FP8: four groups of gate rows, then of up rows; NVFP4: 32 rows, eight of each in turn
 #pragma unroll
     for (int f = 0; f < RF; ++f) at.w[f] = group_at<FP8>(W, FP8 ? c0 + 4 * (f & 3) + (f < 4 ? 0 : I) : 2 * c0 + 4 * f);
     at.block[0] = c0 / 128;
     at.block[1] = (I + c0) / 128;
-    const int row = L.row[u], count = L.count[u];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int c = 4 * j + (r & 3);
-      at.t[j] = c < count ? (uint32_t)L.tok[row + (c < count ? c : 0)] * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
+      at.t[j] = c < (int)y.count ? (uint32_t)y.tok[c] * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
     }
   };
   auto issue = [&](Step& x) {
@@ -478,15 +481,16 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
   float g1 = 1.0f, g2 = 1.0f;   // NVFP4: the global scales of the tile that this wave finishes
   auto start = [&](int unit) {
     if constexpr (!FP8) {
-      const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.e[wave < subs && mine < tiles ? mine / per : 0]);
+      const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.entry[wave < subs && mine < tiles ? mine / per : 0].e);
       g1 = uniform_load(p.gs_w1 + e);
       g2 = uniform_load(p.gs_w2 + e);
     }
-    const int tile = unit * subs + sub, u = tile < tiles ? tile / per : 0, row = L.row[u], count = L.count[u];
+    const int tile = unit * subs + sub;
+    const Entry& y = L.entry[tile < tiles ? tile / per : 0];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int c = 4 * j + (r & 3);
-      if constexpr (!FP8) less[j] = (uint32_t)scale_of(L.tok[row + (c < count ? c : 0)]) * 0x00800080u;
+      if constexpr (!FP8) less[j] = (uint32_t)scale_of(c < (int)y.count ? y.tok[c] : 0) * 0x00800080u;
     }
   };
   auto add = [&](Step& x) {
@@ -548,7 +552,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     const int c = lane & 15, t = lane >> 4, tile = unit * subs + wave;
     const int gate = FP8 ? c : 16 * (c >> 3) + (c & 7), up = gate + (FP8 ? 16 : 8);
     if (tile >= tiles) return;
-    const int u = tile / per, row = L.row[u], count = L.count[u];
+    const int u = tile / per, row = L.entry[u].row, count = (int)L.entry[u].count;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int k = 4 * j + t;
@@ -574,8 +578,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
         }
       } else {
         // back to x's own exponents; a token that is not finite gives NaN
-        const uint32_t top = largest[L.tok[at_row]];
-        const float back = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, scale_of(L.tok[at_row]) - 112);
+        const int tok = L.entry[u].tok[in ? k : 0];
+        const float back = largest[tok] >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, scale_of(tok) - 112);
         a = a * back / g1;
         b = b * back / g1;
         const float h = a / (1.0f + expf(-a)) * b * L.coef[at_row] / g2;
@@ -616,20 +620,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
 //
 // A tile is 4 * RF columns of out, over all entries: a workgroup's waves take the
 // K steps of all entries in turn.  What a step gives its tokens is added to the
-// wave's own sums in LDS, [quarter][token][column], so a token gets nothing from
+// wave's own sums in LDS, [token][quarter][column], so a token gets nothing from
 // experts it did not choose, whatever these hold.
 
-template <bool FP8, int RF, int NG, int kDepth, int kWaves>
-__global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewArgs p) {
+template <bool FP8, int RF, int NG, int kDepth>
+__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
   constexpr int kM = Weights<FP8>::kM, kTok = 4 * NG, kStride = 4 * RF + 4;
   __shared__ Live L;
   __shared__ union {
     LiveScratch build;
-    float sums[kWaves][4][kFewTokens][kStride];
+    float sums[kWaves][kFewTokens][4][kStride];
   } S;
   __shared__ Scales scales[FP8 ? 1 : kWaves];
   if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
-  else build_large<kWaves>(p, kTok, L, S.build);
+  else build_large(p, kTok, L, S.build);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -648,23 +652,12 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewAr
     int cut;                    // FP8: row groups in the tile's first row block
   };
   struct {
-    int i, s, u, b, e;
+    int i, s, u, b;
     int w[RF], block[2], cut;
-    uint32_t t[NG], ex[NG], sc;
-    int tok[NG];
+    uint32_t sc;
+    uint4 y;                    // the entry, read one step before it is used
   } at;
-  auto set_entry = [&]() {
-    const int u = at.u < n ? at.u : 0;
-    at.e = __builtin_amdgcn_readfirstlane(L.e[u]);
-    const int row = L.row[u], count = at.u < n ? L.count[u] : 0;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const int c = 4 * j + (r & 3);
-      at.t[j] = c < count ? (uint32_t)(row + c) * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
-      at.ex[j] = c < count ? (uint32_t)(row + c) * (uint32_t)(W.K / 16) + 8 * (r >> 2) : kNowhere;
-      at.tok[j] = c < count && (r >> 2) == g ? L.tok[row + (c < count ? c : 0)] : -1;
-    }
-  };
+  auto set_entry = [&]() { at.y = *reinterpret_cast<const uint4*>(&L.entry[at.u < n ? at.u : 0]); };
   auto set_tile = [&]() {
     at.s = 0;
     at.u = wave / W.KS;
@@ -680,19 +673,26 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewAr
   };
   auto issue = [&](Step& x) {
     const bool on = at.i < tiles && at.u < n;
-    const uint32_t off = on && W.kCols / 4 * (r >> 2) + W.kCols / 16 * g < W.K - at.b * W.kCols ? 0 : kNowhere;
+    const int col = W.kCols / 4 * (r >> 2) + W.kCols / 16 * g;
     const int so = on ? at.b * W.kCols * 2 : 0;
+    const int e = __builtin_amdgcn_readfirstlane(at.y.x & 0xFFFF), row = at.y.x >> 16;
+    const int count = on && col < W.K - at.b * W.kCols ? (int)at.y.y : 0;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
+      const int c = 4 * j + (r & 3);
+      const bool in = c < count;
+      const uint32_t t = in ? (uint32_t)(row + c) * (uint32_t)W.K * 2 + 2 * col : kNowhere;
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        x.t[j][0][m] = __builtin_amdgcn_raw_buffer_load_b128(rh, (at.t[j] + 16 * m) | off, so, 0);
-        if constexpr (FP8) x.t[j][FP8 ? 1 : 0][m] = __builtin_amdgcn_raw_buffer_load_b128(rl, (at.t[j] + 16 * m) | off, so, 0);
+        x.t[j][0][m] = __builtin_amdgcn_raw_buffer_load_b128(rh, t + 16 * m, so, 0);
+        if constexpr (FP8) x.t[j][FP8 ? 1 : 0][m] = __builtin_amdgcn_raw_buffer_load_b128(rl, t + 16 * m, so, 0);
       }
-      if constexpr (!FP8) x.ex[j] = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rl, at.ex[j] | off, on ? at.b * 32 : 0, 0));
-      x.tok[j] = at.tok[j];
+      if constexpr (!FP8)
+        x.ex[j] = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rl, in ? (uint32_t)(row + c) * (uint32_t)(W.K / 16) + 8 * (r >> 2) : kNowhere, on ? at.b * 32 : 0, 0));
+      // a lane of equal quarters has its token's results, in or behind K
+      x.tok[j] = on && c < (int)at.y.y && (r >> 2) == g ? (int)((j ? at.y.w : at.y.z) >> (8 * (r & 3)) & 255) : -1;
     }
-    load_weights<FP8, RF, false>(W, at.e, at.w, at.block, at.sc, at.b, on, lane, x.w);
+    load_weights<FP8, RF, false>(W, e, at.w, at.block, at.sc, at.b, on, lane, x.w);
     x.cut = at.cut;
     asm volatile("" ::: "memory");                       // issued here, not where they are used
     if (++at.s == steps) {
@@ -751,7 +751,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewAr
       for (int j = 0; j < NG; ++j) {
         if (x.tok[j] < 0) continue;
         const float sc = !FP8 ? back[j] : f < x.cut ? s0 : s1;
-        float4v* to = reinterpret_cast<float4v*>(&S.sums[wave][g][x.tok[j]][4 * f]);
+        float4v* to = reinterpret_cast<float4v*>(&S.sums[wave][x.tok[j]][g][4 * f]);
         float4v v = *to;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = fmaf(d[j][i], sc, v[i]);
@@ -761,7 +761,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewAr
   };
   auto clear = [&]() {
     float4v* own = reinterpret_cast<float4v*>(&S.sums[wave][0][0][0]);
-    for (int i = lane; i < 4 * kFewTokens * kStride / 4; i += 64) own[i] = float4v{0, 0, 0, 0};
+    for (int i = lane; i < T * kStride; i += 64) own[i] = float4v{0, 0, 0, 0};
   };
   // the tile's sums over waves and quarters, and out
   auto finish = [&](int i) {
@@ -771,7 +771,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 4) void few_down_kernel(FewAr
       const int t = o / (4 * RF), c = o - t * (4 * RF);
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += S.sums[w][q][t][c];
+      for (int w = 0; w < kWaves; ++w) v += S.sums[w][t][q][c];
       v += __shfl_xor(v, 1);
       v += __shfl_xor(v, 2);
       if (q == 0 && 4 * RF * i + c < H) p.out[(int64_t)t * H + 4 * RF * i + c] = (uint16_t)pack_bf16x2(v, 0.0f);
@@ -827,8 +827,7 @@ hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
   auto down = [&](auto rf) {
     constexpr int RF = decltype(rf)::value;
     const int64_t t = up(a.H, 4 * RF);
-    constexpr int waves = RF <= 4 && NG == 1 ? 16 : 8;
-    few_down_kernel<FP8, RF, NG, 2, waves><<<(unsigned)(t < cus ? t : cus), waves * 64, 0, stream>>>(a);
+    few_down_kernel<FP8, RF, NG, 2><<<(unsigned)(t < cus ? t : cus), kThreads, 0, stream>>>(a);
   };
   if (a.H <= 8 * cus) down(std::integral_constant<int, 2>{});
   else if (a.H <= 16 * cus) down(std::integral_constant<int, 4>{});
