@@ -117,8 +117,9 @@ __device__ __forceinline__ void put_entries(Live& L, int e, int rows, int row, i
 __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
   if (threadIdx.x < 64) {
     const int pairs = p.T * p.k, lane = threadIdx.x;
-    const int e = lane < pairs ? p.ids[lane] : -1, t = lane / p.k;
+    const int e = lane < pairs ? p.ids[lane] : -1;
     const float w = lane < pairs ? p.topk_w[lane] : 0.0f;
+    const int t = (int)(((float)lane + 0.5f) * __builtin_amdgcn_rcpf((float)p.k));   // lane / k: never within 2^-7 of a whole number
     const bool on = e >= 0 && e < p.E;
     int *mask_of = S.mask, *first_of = S.row, *count_of = S.id;
     mask_of[lane] = 0;
@@ -242,30 +243,31 @@ __device__ void build_large(const FewArgs& p, int cap, Live& L, LiveScratch& S) 
   __syncthreads();
 }
 
-// One operand of a product: the weights of all experts, N rows of K.
-template <bool FP8>
+// One operand of a product: the weights of all experts, N rows of K.  Sizes and
+// counts come from the host: a kernel that runs for some microseconds has no time
+// for divisions.
 struct Weights {
-  static constexpr int kCols = FP8 ? 256 : 512;          // a K step
-  static constexpr int kM = FP8 ? 2 : 4;                 // its matrix instructions a row group
   const uint8_t* q;
   const uint8_t* sf;            // FP8: float scales
-  int K, KB, KS;                // scale blocks or stages of 128, K steps
+  int N, K, KB, KS;             // KB: scale blocks or stages of 128; KS: K steps
   int64_t q_bytes, sf_bytes;    // of one expert
 };
 
 template <bool FP8>
-__device__ __forceinline__ Weights<FP8> weights_of(const uint8_t* q, const void* sf, int64_t N, int64_t K) {
-  Weights<FP8> w;
-  w.q = q;
-  w.sf = static_cast<const uint8_t*>(sf);
-  w.K = (int)K;
-  w.KB = (int)((K + 127) / 128);
-  w.KS = (int)((K + w.kCols - 1) / w.kCols);
-  const int64_t Np = (N + NVFP4_PACK_ROWS - 1) / NVFP4_PACK_ROWS * NVFP4_PACK_ROWS;
-  w.q_bytes = FP8 ? N * K : Np * (K / 2);
-  w.sf_bytes = FP8 ? (N + 127) / 128 * w.KB * 4 : Np * (K / 16);
-  return w;
-}
+struct Format {
+  static constexpr int kCols = FP8 ? 256 : 512;          // a K step
+  static constexpr int kM = FP8 ? 2 : 4;                 // its matrix instructions a row group
+};
+
+struct FewParams {
+  FewArgs a;
+  Weights w;                    // w1 (up) or w2 (down)
+  int split;                    // up: log2 of the waves a tile
+  int tiles;                    // up: of one entry; down: all
+  float inv_tiles;              // up: 1 / tiles
+  int steps;                    // up: K steps a wave
+  int64_t t_bytes;              // of x or of one plane of h
+};
 
 // A lane holds, of weight row group f (4 rows), row r & 3 and of quarter r >> 2
 // the 16 bytes g (r = lane & 15, g = lane >> 4); of token group j, token r & 3 and
@@ -279,7 +281,7 @@ struct StepW {
 
 // Where row group f of a tile begins in one expert's weights, in bytes, K step 0.
 template <bool FP8>
-__device__ __forceinline__ int group_at(const Weights<FP8>& W, int row) {
+__device__ __forceinline__ int group_at(const Weights& W, int row) {
   return FP8 ? row * W.K : ((row / NVFP4_PACK_ROWS) * W.KB * NVFP4_PACK_ROWS + row % NVFP4_PACK_ROWS) * 64;
 }
 
@@ -290,7 +292,7 @@ __device__ __forceinline__ int group_at(const Weights<FP8>& W, int row) {
 // quarter q: stages are 32 KiB apart, so one group's quarters would all come from
 // one memory channel (sixteen tokens, first product: 327 us, turned 308).
 template <bool FP8, int RF, bool TURN>
-__device__ __forceinline__ void load_weights(const Weights<FP8>& W, int e, const int (&at)[RF], const int (&block)[2],
+__device__ __forceinline__ void load_weights(const Weights& W, int e, const int (&at)[RF], const int (&block)[2],
                                              uint32_t scale_at, int b, bool on, int lane, StepW<FP8, RF>& x) {
   const int r = lane & 15, g = lane >> 4, q = r >> 2;
   const auto rq = rsrc_of(W.q + e * W.q_bytes, W.q_bytes);
@@ -383,8 +385,10 @@ __device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
 // tile ends, kDepth steps ahead.
 
 template <bool FP8, int NG, int kDepth>
-__global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int split) {
-  constexpr int RF = 8, kM = Weights<FP8>::kM, kTok = 4 * NG;
+__global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
+  constexpr int RF = 8, kCols = Format<FP8>::kCols, kM = Format<FP8>::kM, kTok = 4 * NG;
+  const FewArgs& p = P.a;
+  const Weights& W = P.w;
   __shared__ Live L;
   __shared__ union {
     LiveScratch build;
@@ -412,14 +416,18 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
   if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
   else build_large(p, kTok, L, S.build);
 
-  const int subs = kWaves / split, sub = wave / split, part = wave - sub * split;
-  const int I = (int)p.I, per = I / 16, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
-  const int units = (tiles + subs - 1) / subs, stride = gridDim.x;
+  const int split = 1 << P.split, subs = kWaves >> P.split, sub = wave >> P.split, part = wave & (split - 1);
+  const int I = W.N / 2, per = P.tiles, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
+  const int units = (tiles + subs - 1) >> (3 - P.split), stride = gridDim.x, steps = P.steps;
   if ((int)blockIdx.x >= units) return;
-  const auto W = weights_of<FP8>(p.w1_q, p.w1_sf, 2 * p.I, p.H);
-  const int steps = (W.KS + split - 1) / split;
-  const int total = ((units - 1 - (int)blockIdx.x) / stride + 1) * steps;
-  const auto rx = rsrc_of(p.x, (int64_t)p.T * p.H * 2);
+  const auto rx = rsrc_of(p.x, P.t_bytes);
+  const int lane_col = kCols / 4 * (r >> 2) + kCols / 16 * g;   // of this lane's tokens in a K step
+  // the entry of a tile: its quotient by `per` to one, then put right
+  auto entry_of = [&](int tile) {
+    int u = __builtin_amdgcn_readfirstlane((int)((float)tile * P.inv_tiles));
+    const int left = tile - u * per;
+    return u + (left >= per ? 1 : 0) - (left < 0 ? 1 : 0);
+  };
 
   struct Step {
     StepW<FP8, RF> w;
@@ -432,7 +440,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     uint32_t t[NG], sc;         // this lane's tokens' bytes, and place in the scales
   } at;
   auto set_tile = [&]() {
-    const int tile = at.i * subs + sub, u = tile < tiles ? tile / per : 0;
+    const int tile = at.i * subs + sub, u = tile < tiles ? entry_of(tile) : 0;
     at.on = tile < tiles;
     at.s = 0;
     at.b = part;
@@ -448,13 +456,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int c = 4 * j + (r & 3);
-      at.t[j] = c < (int)y.count ? (uint32_t)y.tok[c] * (uint32_t)W.K * 2 + 2 * (W.kCols / 4 * (r >> 2) + W.kCols / 16 * g) : kNowhere;
+      at.t[j] = c < (int)y.count ? (uint32_t)y.tok[c] * (uint32_t)W.K * 2 + 2 * lane_col : kNowhere;
     }
   };
   auto issue = [&](Step& x) {
     const bool on = at.on && at.b < W.KS;
-    const uint32_t off = on && W.kCols / 4 * (r >> 2) + W.kCols / 16 * g < W.K - at.b * W.kCols ? 0 : kNowhere;
-    const int so = on ? at.b * W.kCols * 2 : 0;
+    const uint32_t off = on && lane_col < W.K - at.b * kCols ? 0 : kNowhere;
+    const int so = on ? at.b * kCols * 2 : 0;
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -481,12 +489,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
   float g1 = 1.0f, g2 = 1.0f;   // NVFP4: the global scales of the tile that this wave finishes
   auto start = [&](int unit) {
     if constexpr (!FP8) {
-      const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.entry[wave < subs && mine < tiles ? mine / per : 0].e);
+      const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.entry[wave < subs && mine < tiles ? entry_of(mine) : 0].e);
       g1 = uniform_load(p.gs_w1 + e);
       g2 = uniform_load(p.gs_w2 + e);
     }
     const int tile = unit * subs + sub;
-    const Entry& y = L.entry[tile < tiles ? tile / per : 0];
+    const Entry& y = L.entry[tile < tiles ? entry_of(tile) : 0];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int c = 4 * j + (r & 3);
@@ -552,7 +560,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
     const int c = lane & 15, t = lane >> 4, tile = unit * subs + wave;
     const int gate = FP8 ? c : 16 * (c >> 3) + (c & 7), up = gate + (FP8 ? 16 : 8);
     if (tile >= tiles) return;
-    const int u = tile / per, row = L.entry[u].row, count = (int)L.entry[u].count;
+    const int u = entry_of(tile), row = L.entry[u].row, count = (int)L.entry[u].count;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int k = 4 * j + t;
@@ -600,17 +608,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
   for (int d = 0; d < kDepth; ++d) issue(x[d]);
   int unit = blockIdx.x, s = 0;
   start(unit);
-  for (int q = 0;; q += kDepth) {
+  for (;;) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (q + d >= total) return;
       add(x[d]);
       issue(x[d]);
       if (++s == steps) {
         finish(unit);
         unit += stride;
+        if (unit >= units) return;
         s = 0;
-        if (q + d + 1 < total) start(unit);
+        start(unit);
       }
     }
   }
@@ -624,8 +632,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewArgs p, int spli
 // experts it did not choose, whatever these hold.
 
 template <bool FP8, int RF, int NG, int kDepth>
-__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
-  constexpr int kM = Weights<FP8>::kM, kTok = 4 * NG, kStride = 4 * RF + 4;
+__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
+  constexpr int kCols = Format<FP8>::kCols, kM = Format<FP8>::kM, kTok = 4 * NG, kStride = 4 * RF + 4;
+  const FewArgs& p = P.a;
+  const Weights& W = P.w;
   __shared__ Live L;
   __shared__ union {
     LiveScratch build;
@@ -638,11 +648,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n = __builtin_amdgcn_readfirstlane(L.n), stride = gridDim.x, T = p.T;
-  const int H = (int)p.H, tiles = (H + 4 * RF - 1) / (4 * RF);
-  const auto W = weights_of<FP8>(p.w2_q, p.w2_sf, p.H, p.I);
+  const int H = W.N, tiles = P.tiles;
   const int steps = (n * W.KS + kWaves - 1) / kWaves;
-  const int64_t plane = (int64_t)T * p.k * p.I * 2;
-  const auto rh = rsrc_of(p.h_hi, plane), rl = rsrc_of(p.h_lo, FP8 ? plane : plane / 32);
+  const auto rh = rsrc_of(p.h_hi, P.t_bytes), rl = rsrc_of(p.h_lo, FP8 ? P.t_bytes : P.t_bytes / 32);
+  const int lane_col = kCols / 4 * (r >> 2) + kCols / 16 * g;   // of this lane's tokens in a K step
 
   struct Step {
     StepW<FP8, RF> w;
@@ -660,8 +669,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
   auto set_entry = [&]() { at.y = *reinterpret_cast<const uint4*>(&L.entry[at.u < n ? at.u : 0]); };
   auto set_tile = [&]() {
     at.s = 0;
-    at.u = wave / W.KS;
-    at.b = wave - at.u * W.KS;
+    at.u = 0;
+    for (at.b = wave; at.b >= W.KS; at.b -= W.KS) ++at.u;
     const int row0 = 4 * RF * at.i;
     at.sc = scale_place<RF>(row0, H, W.KB, lane);
 #pragma unroll
@@ -673,15 +682,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
   };
   auto issue = [&](Step& x) {
     const bool on = at.i < tiles && at.u < n;
-    const int col = W.kCols / 4 * (r >> 2) + W.kCols / 16 * g;
-    const int so = on ? at.b * W.kCols * 2 : 0;
+    const int so = on ? at.b * kCols * 2 : 0;
     const int e = __builtin_amdgcn_readfirstlane(at.y.x & 0xFFFF), row = at.y.x >> 16;
-    const int count = on && col < W.K - at.b * W.kCols ? (int)at.y.y : 0;
+    const int count = on && lane_col < W.K - at.b * kCols ? (int)at.y.y : 0;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const int c = 4 * j + (r & 3);
       const bool in = c < count;
-      const uint32_t t = in ? (uint32_t)(row + c) * (uint32_t)W.K * 2 + 2 * col : kNowhere;
+      const uint32_t t = in ? (uint32_t)(row + c) * (uint32_t)W.K * 2 + 2 * lane_col : kNowhere;
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         x.t[j][0][m] = __builtin_amdgcn_raw_buffer_load_b128(rh, t + 16 * m, so, 0);
@@ -790,44 +798,65 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
     for (int i = blockIdx.x; i < tiles; i += stride) finish(i);
     return;
   }
-  const int total = ((tiles - 1 - (int)blockIdx.x) / stride + 1) * steps;
   int i = blockIdx.x, s = 0;
-  for (int q = 0;; q += kDepth) {
+  for (;;) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (q + d >= total) return;
       add(x[d]);
       issue(x[d]);
       if (++s == steps) {
         finish(i);
         i += stride;
+        if (i >= tiles) return;
         s = 0;
       }
     }
   }
 }
 
+template <bool FP8>
+Weights weights_of(const uint8_t* q, const void* sf, int64_t N, int64_t K) {
+  Weights w;
+  w.q = q;
+  w.sf = static_cast<const uint8_t*>(sf);
+  w.N = (int)N;
+  w.K = (int)K;
+  w.KB = (int)((K + 127) / 128);
+  w.KS = (int)((K + Format<FP8>::kCols - 1) / Format<FP8>::kCols);
+  w.q_bytes = FP8 ? N * K : packed_rows(N) * (K / 2);
+  w.sf_bytes = FP8 ? (N + 127) / 128 * w.KB * 4 : packed_rows(N) * (K / 16);
+  return w;
+}
+
 template <bool FP8, int NG>
 hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const int64_t pairs = (int64_t)a.T * a.k, live = pairs < a.E ? pairs : a.E;
+  FewParams p;
+  p.a = a;
+  p.w = weights_of<FP8>(a.w1_q, a.w1_sf, 2 * a.I, a.H);
+  p.tiles = (int)(a.I / 16);
+  p.inv_tiles = 1.0f / (float)p.tiles;
+  p.t_bytes = (int64_t)a.T * a.H * 2;
   // Waves a tile of the first product: the fewest rounds of its K steps, the join
   // of several waves counted as two steps, a wave's own end of a tile as one.
-  const int64_t tiles = live * (a.I / 16), ks = (a.H + Weights<FP8>::kCols - 1) / Weights<FP8>::kCols;
-  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-  int split = kWaves;
+  const int64_t tiles = live * p.tiles;
   int64_t best = INT64_MAX;
-  for (int s = kWaves; s >= 1; s /= 2) {
-    const int64_t c = up(up(tiles * s, kWaves), cus) * (up(ks, s) + (s > 1 ? 2 : 1));
-    if (c < best) { best = c; split = s; }
+  for (int s = 3; s >= 0; --s) {
+    const int64_t c = up(up(tiles << s, kWaves), cus) * (up(p.w.KS, 1 << s) + (s > 0 ? 2 : 1));
+    if (c < best) { best = c; p.split = s; }
   }
-  const int64_t units = up(tiles * split, kWaves);
-  few_up_kernel<FP8, NG, 2><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(a, split);
-  hipError_t err = hipGetLastError();
+  p.steps = (int)up(p.w.KS, 1 << p.split);
+  const int64_t units = up(tiles << p.split, kWaves);
+  few_up_kernel<FP8, NG, 2><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(p);
+  const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  p.w = weights_of<FP8>(a.w2_q, a.w2_sf, a.H, a.I);
+  p.t_bytes = pairs * a.I * 2;
   auto down = [&](auto rf) {
     constexpr int RF = decltype(rf)::value;
-    const int64_t t = up(a.H, 4 * RF);
-    few_down_kernel<FP8, RF, NG, 2><<<(unsigned)(t < cus ? t : cus), kThreads, 0, stream>>>(a);
+    p.tiles = (int)up(a.H, 4 * RF);
+    few_down_kernel<FP8, RF, NG, 2><<<p.tiles < cus ? p.tiles : cus, kThreads, 0, stream>>>(p);
   };
   if (a.H <= 8 * cus) down(std::integral_constant<int, 2>{});
   else if (a.H <= 16 * cus) down(std::integral_constant<int, 4>{});
