@@ -765,23 +765,25 @@ def _norm_weight(w, H):
 
 def _rmsnorm(x, w, residual, eps, y, q, sf, h, rstd, need_y, need_q, need_rstd):
     _rows_of(x, "x")
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     wide = _norm_weight(w, H)
+    r, ld_r = None, 0
     if residual is not None:
         _rows_of(residual, "residual")
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError(f"residual must have shape {(T, H)} (got {tuple(residual.shape)})")
-        h = _out(h, (T, H), torch.bfloat16, x, "h")
+        h = _out(h, shape, torch.bfloat16, x, "h")
+        r, ld_r = residual.data_ptr(), _ld(residual)
     elif h is not None:
         raise ValueError("h is x without a residual: no tensor to write it to")
-    y = _out(y, (T, H), torch.bfloat16, x, "y") if need_y else None
+    y = _out(y, shape, torch.bfloat16, x, "y") if need_y else None
     if need_q:
-        q = _out(q, (T, H), FP8, x, "q")
+        q = _out(q, shape, FP8, x, "q")
         sf = _out(sf, (T, _scale_blocks(H)), torch.float32, x, "sf")
     rstd = _out(rstd, (T,), torch.float32, x, "rstd") if need_rstd else None
-    _call("nvfp4_rmsnorm", (x, residual, w, h, y, q, sf, rstd), _ptr(x), _ld(x), _ptr(residual),
-          _ld(residual) if residual is not None else 0, _ptr(w), wide, T, H, eps, _ptr(h), _ptr(y), _ptr(q),
-          _ptr(sf), _ptr(rstd))
+    _call("nvfp4_rmsnorm", (x, residual, w, h, y, q, sf, rstd), x.data_ptr(), _ld(x), r, ld_r, w.data_ptr(), wide, T,
+          H, eps, _ptr(h), _ptr(y), _ptr(q), _ptr(sf), _ptr(rstd))
     return y, q, sf, x if residual is None else h, rstd
 
 
@@ -826,16 +828,19 @@ def rmsnorm_bwd(dy, h, w, rstd, dh=None, need_dw=True, out=None, workspace=None)
     dx, dw = out if out is not None else (None, None)
     dx = _out(dx, (T, H), torch.bfloat16, dy, "dx")
     ws = None
+    n = 0
     if need_dw:
         dw = _out(dw, (H,), torch.float32, dy, "dw")
-        ws = workspace
-        if ws is None:
-            ws = _workspace(lib().nvfp4_rmsnorm_bwd_workspace_size(T, H), dy.device)
-        _is(ws, torch.uint8, "workspace")
+        if workspace is None:
+            n = lib().nvfp4_rmsnorm_bwd_workspace_size(T, H)
+            ws = dy.new_empty(n, dtype=torch.uint8)
+        else:
+            ws = _is(workspace, torch.uint8, "workspace")
+            n = ws.numel()
     else:
         dw = None
-    _call("nvfp4_rmsnorm_bwd", (dy, dh, h, rstd, w, dx, dw, ws), _ptr(dy), _ptr(dh), _ptr(h), _ptr(rstd), _ptr(w),
-          wide, T, H, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() if ws is not None else 0)
+    _call("nvfp4_rmsnorm_bwd", (dy, dh, h, rstd, w, dx, dw, ws), dy.data_ptr(), _ptr(dh), h.data_ptr(),
+          rstd.data_ptr(), w.data_ptr(), wide, T, H, dx.data_ptr(), _ptr(dw), _ptr(ws), n)
     return dx, dw
 
 
@@ -849,12 +854,14 @@ def _few(name, x, topk_ids, topk_w, H, I, E, weights, out, workspace):
     _is(topk_ids, torch.int32, "topk_ids", (T, k))
     _is(topk_w, torch.float32, "topk_w", (T, k))
     o = _out(out, (T, H), torch.bfloat16, x)
-    ws = workspace
-    if ws is None:
-        ws = _workspace(lib().moe_expert_forward_few_workspace_size(T, I, k), x.device)
-    _is(ws, torch.uint8, "workspace")
-    _call(name, (x, topk_ids, topk_w, *weights, o, ws), _ptr(x), T, H, I, E, k, _ptr(topk_ids), _ptr(topk_w),
-          *[t.data_ptr() for t in weights], _ptr(o), _ptr(ws), ws.numel())
+    if workspace is None:
+        n = lib().moe_expert_forward_few_workspace_size(T, I, k)
+        ws = x.new_empty(n, dtype=torch.uint8)
+    else:
+        ws = _is(workspace, torch.uint8, "workspace")
+        n = ws.numel()
+    _call(name, (x, topk_ids, topk_w, *weights, o, ws), x.data_ptr(), T, H, I, E, k, topk_ids.data_ptr(),
+          topk_w.data_ptr(), *[t.data_ptr() for t in weights], o.data_ptr(), ws.data_ptr(), n)
     return o
 
 
@@ -872,13 +879,12 @@ def moe_expert_forward_few(x, topk_ids, topk_w, w: ExpertWeights, out=None, work
     E, H, I = w.E, w.H, w.I
     if w.w2.N != H or w.w2.K != I or w.w2.E != E:
         raise ValueError("weight shapes do not match")
-    L = lib()
-    sf = c_size_t(0)
-    for p, name in ((w.w1, "w1"), (w.w2, "w2")):
-        _is(p.q, torch.uint8, name + ".q")
-        _is(p.sf, torch.uint8, name + ".sf")
-        if p.q.numel() < L.nvfp4_packed_weight_bytes(E, p.N, p.K, ctypes.byref(sf)) or p.sf.numel() < sf.value:
-            raise ValueError(f"{name} holds less than its packed experts")
+    for p in (w.w1, w.w2):
+        _is(p.q, torch.uint8, "q")
+        _is(p.sf, torch.uint8, "sf")
+        rows = E * ((p.N + 511) // 512 * 512)             # nvfp4_packed_weight_bytes
+        if p.q.numel() < rows * (p.K // 2) or p.sf.numel() < rows * (p.K // 16):
+            raise ValueError("the weights hold less than their packed experts")
     _is(w.gs_w1, torch.float32, "gs_w1", (E,))
     _is(w.gs_w2, torch.float32, "gs_w2", (E,))
     return _few("moe_expert_forward_few", x, topk_ids, topk_w, H, I, E,

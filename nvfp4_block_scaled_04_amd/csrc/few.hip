@@ -486,12 +486,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
     const int e = (int)(largest[t] >> 7) - 30;
     return e > 0 ? e : 0;
   };
-  float g1 = 1.0f, g2 = 1.0f;   // NVFP4: the global scales of the tile that this wave finishes
+  float r1 = 1.0f, r2 = 1.0f;   // NVFP4: 1 / the global scales of the tile that this wave finishes
   auto start = [&](int unit) {
     if constexpr (!FP8) {
       const int mine = unit * subs + wave, e = __builtin_amdgcn_readfirstlane(L.entry[wave < subs && mine < tiles ? entry_of(mine) : 0].e);
-      g1 = uniform_load(p.gs_w1 + e);
-      g2 = uniform_load(p.gs_w2 + e);
+      r1 = 1.0f / uniform_load(p.gs_w1 + e);
+      r2 = 1.0f / uniform_load(p.gs_w2 + e);
     }
     const int tile = unit * subs + sub;
     const Entry& y = L.entry[tile < tiles ? entry_of(tile) : 0];
@@ -565,6 +565,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
     for (int j = 0; j < NG; ++j) {
       const int k = 4 * j + t;
       float a = 0.0f, b = 0.0f;
+#pragma unroll 2
       for (int w = wave * split; w < (wave + 1) * split; ++w) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -588,9 +589,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
         // back to x's own exponents; a token that is not finite gives NaN
         const int tok = L.entry[u].tok[in ? k : 0];
         const float back = largest[tok] >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, scale_of(tok) - 112);
-        a = a * back / g1;
-        b = b * back / g1;
-        const float h = a / (1.0f + expf(-a)) * b * L.coef[at_row] / g2;
+        a = a * back * r1;
+        b = b * back * r1;
+        const float h = a / (1.0f + expf(-a)) * b * L.coef[at_row] * r2;
         const int ex = __float_as_uint(max16(fabsf(h))) >> 23;
         const _Float16 v = (_Float16)ldexpf(h, 141 - ex);   // the 16 columns' largest: 2^14 .. 2^15
         if (in) {
