@@ -987,7 +987,7 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, co
   if (st != NVFP4_OK) return st;
   if (w_fp32 != 0 && w_fp32 != 1) return fail(NVFP4_ERR_INVALID_ARG, "w_fp32 must be 0 or 1 (got %d)", w_fp32);
   if (rows == 0 && !dw) return NVFP4_OK;
-  if (rows > 0 && (!dy || !h || !rstd || !w || !dx))
+  if (!w || (rows > 0 && (!dy || !h || !rstd || !dx)))
     return fail(NVFP4_ERR_INVALID_ARG, "dy, h, rstd, w and dx must be non-NULL");
   if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
       !aligned(rstd, 4) || !aligned(dw, 4))

@@ -58,6 +58,7 @@ def _bwd(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), -2), (dict(rows=1 << 31), -2), (dict(cols=4), -2), (dict(cols=32776), -2), (dict(wide=-1), -1),
     (dict(dy=None), -1), (dict(h=None), -1), (dict(rstd=None), -1), (dict(w=None), -1), (dict(dx=None), -1),
+    (dict(rows=0, w=None), -1),                           # dw of no rows is written all the same
     (dict(ws=None), -3), (dict(wsb=64), -3), (dict(ws=P[7] + 8), -3), (dict(rows=0, ws=None), -3),
     (dict(dy=P[0] + 8), -1), (dict(dh=P[1] + 8), -1), (dict(h=P[2] + 8), -1), (dict(w=P[4] + 8), -1),
     (dict(dx=P[5] + 8), -1), (dict(rstd=P[3] + 2), -1), (dict(dw=P[6] + 2), -1),
