@@ -546,7 +546,7 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64
  * nullable, but one of y and q is needed.  h may be x or residual itself
  * (rows contiguous).  Rows whose mean of h^2 passes the largest fp32 give 0.
  * Shapes: rows in [0, 2^31); cols % 8 == 0 (with q: % 16), 8 <= cols <= 32768;
- *   ld_x, ld_r >= cols and multiples of 8; eps > 0.  No workspace.
+ *   ld_x, ld_r >= cols and multiples of 8; eps >= 1e-30.  No workspace.
  *
  * nvfp4_rmsnorm_bwd: dy the gradient of v (of y, or straight through the FP8
  * rounding), dh (nullable) that of h from elsewhere, h and rstd as the forward
@@ -575,8 +575,9 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const v
  *   [gate | up] = W1[e] x[t],   h = silu(gate) * up   (fp32),
  *   out[t] = bf16_rne( sum_j topk_w[t][j] * W2[e] h ),
  * products and sums in fp32, each h rounded to 11 bits of significand or more (and
- * to 2^-39 of the largest of 128).  Ids
- * outside [0, E) contribute nothing (a token with none but these gives zeros);
+ * to 2^-39 of the largest of 128).  With NVFP4 weights what lies below 2^-29 of the
+ * token's largest |x| is lost, and a token that holds an infinity or NaN gives NaN.
+ * Ids outside [0, E) contribute nothing (a token with none but these gives zeros);
  * an id may come twice in a row.  A shared expert is a further expert and a
  * further slot of weight 1.  Each live expert's weights are read once.
  * x, out BF16 [T][H]; topk_ids int32, topk_w float [T][k].

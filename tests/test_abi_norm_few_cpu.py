@@ -30,7 +30,7 @@ def _norm(**kw):
     (dict(cols=32776, ld_x=32776, ld_r=32776), -2), (dict(cols=24), -2),              # FP8 of 24 columns
     (dict(ld_x=56), -2), (dict(ld_r=60), -2), (dict(ld_x=68), -2), (dict(ld_x=1 << 40), -2),
     (dict(rows=(1 << 31) - 1, ld_r=(1 << 40) - 8), -2),
-    (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
+    (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1), (dict(eps=9e-31), -1),
     (dict(wide=2), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(y=None, q=None, sf=None), -1),
     (dict(sf=None), -1), (dict(q=None), -1), (dict(h=None), -1), (dict(res=None), -1),
     (dict(x=P[0] + 8), -1), (dict(res=P[1] + 2), -1), (dict(w=P[2] + 4), -1), (dict(h=P[3] + 8), -1),

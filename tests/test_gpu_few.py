@@ -138,6 +138,76 @@ def test_few_bad_rows_and_experts_stay_their_own(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_few_magnitudes(fmt):
+    """Tokens of sizes far apart in one call: each as exact as alone."""
+    rng = np.random.default_rng(14)
+    make, call = MAKE[fmt]
+    args, w1, w2 = make(rng, 5, 640, 256)
+    scale = torch.tensor([1e-15, 1e-9, 1e-4, 1.0, 0.0, 1e4, 1e9, 1e15, 3.0])[:, None]
+    x = (_bf(rng, 9, 640).float() * scale).to(torch.bfloat16)
+    x[8, ::3] *= 2.0 ** -12                               # and far apart in one token
+    ids, w = _routing(rng, 9, 5, 3)
+    out = call(x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), *args)
+    _check(out, x, ids, w, w1, w2)
+    assert torch.all(out[4] == 0)
+
+
+def test_few_infinite_tokens_are_nan():
+    rng = np.random.default_rng(15)
+    args, w1, w2 = _nvfp4_weights(rng, 4, 256, 128)
+    x = _bf(rng, 6, 256)
+    x[1, 5], x[4, 250] = float("inf"), float("-inf")
+    ids, w = _routing(rng, 6, 4, 2)
+    out = nv.moe_expert_forward_few(x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), *args)
+    keep = [0, 2, 3, 5]
+    _check(out[keep], x[keep], ids[keep], w[keep], w1, w2)
+    assert torch.isnan(out[[1, 4]].float()).all()
+
+
+@pytest.mark.parametrize("E,k", [(4096, 8), (3000, 4), (5, 33)])
+def test_few_lists_of_many_pairs(E, k):
+    """More than 64 pairs: the other way of making the list of experts."""
+    rng = np.random.default_rng(E + k)
+    args, w1, w2 = _fp8_weights(rng, E, 32, 16)
+    x = _bf(rng, 16, 32)
+    ids, w = _routing(rng, 16, E, k, 0.1)
+    ids[3, 0], ids[3, 1], ids[5, 2] = 0, E - 1, E         # the ends, and one past them
+    out = nv.moe_expert_forward_few_fp8(x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), *args)
+    _check(out, x, np.where(ids >= E, -1, ids), w, w1, w2)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_few_two_graphs_one_workspace(fmt):
+    """Two layers captured apart on one workspace, replayed in turn on one stream
+    with eager calls between."""
+    rng = np.random.default_rng(16)
+    make, call = MAKE[fmt]
+    layers = [make(rng, 6, 384, 128) for _ in range(2)]
+    x = [_bf(rng, T, 384) for T in (4, 11)]
+    routes = [_routing(rng, T, 6, 3, 0.1) for T in (4, 11)]
+    dev = [(a.to(DEV), torch.from_numpy(i).to(DEV), torch.from_numpy(v).to(DEV)) for a, (i, v) in zip(x, routes)]
+    ws = nv.few_workspace(16, 128, 3, DEV)
+    outs = [torch.empty(a.shape, dtype=torch.bfloat16, device=DEV) for a in x]
+    graphs = []
+    for j in range(2):
+        call(*dev[j], *layers[j][0], out=outs[j], workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(*dev[j], *layers[j][0], out=outs[j], workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        call(*dev[0], *layers[1][0], workspace=ws)
+        torch.cuda.synchronize()
+        for j in range(2):
+            _check(outs[j], x[j], *routes[j], layers[j][1], layers[j][2])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
 def test_few_repeats_and_slots(fmt):
     """Equal inputs give equal bits; an id twice in a row counts with both weights;
     a slot of weight 0 changes nothing but the sign of zeros."""
