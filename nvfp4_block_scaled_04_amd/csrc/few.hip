@@ -42,7 +42,6 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kDepth = 2;                             // K steps in flight a wave: more cost their issue up front
 constexpr int kPairs = kFewTokens * 64;               // (token, slot) pairs at most
 constexpr int kMaxExperts = 4096;
 
@@ -113,12 +112,14 @@ __device__ __forceinline__ void put_entries(Live& L, int e, int rows, int row, i
   }
 }
 
-// At most 64 pairs: one wave, a lane a pair.  Pairs of one expert find each other
+// At most 64 pairs: one wave, a lane a pair, the last wave, which has no token's
+// largest to find where there are fewer than eight (NVFP4, one token: the first
+// product 29.6 -> 28.7 us, of the small layer 9.8 -> 9.1).  Pairs of one expert find each other
 // by writing their lane to the expert's place: whichever stays there collects for
 // all of them.
 __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, LiveScratch& S) {
-  if (threadIdx.x < 64) {
-    const int pairs = p.T * p.k, lane = threadIdx.x;
+  if (threadIdx.x >= kThreads - 64) {
+    const int pairs = p.T * p.k, lane = threadIdx.x & 63;
     const int e = lane < pairs ? p.ids[lane] : -1;
     const float w = lane < pairs ? p.topk_w[lane] : 0.0f;
     const int t = (int)(((float)lane + 0.5f) * __builtin_amdgcn_rcpf((float)p.k));   // lane / k: never within 2^-7 of a whole number
@@ -384,14 +385,18 @@ __device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
 // A tile is 16 columns of h of one entry: their 16 gate and 16 up rows.  `split`
 // waves of a workgroup take its K steps in turn and join through LDS; the
 // workgroup works on 8 / split tiles at a time, and a wave's loads run on across
-// tile ends, kDepth steps ahead.  Alone with its tile a wave needs no barrier.
+// tile ends: a step's go out before the one in front of it is added, so that two are
+// in flight.  Alone with its tile a wave needs no barrier.
 //
 // Measured, one MI355X, H 7168, I 2048, 8 of 256 experts a token: one token FP8 38
 // to 40 us (235 MB), NVFP4 28 to 30 us (132 MB), of which 2.6 us are an empty
 // launch, 1 the list, 3 the way to the first weights and 2 the end; sixteen tokens
 // (102 experts) FP8 455 to 490 us (6.1 to 6.5 TB/s), NVFP4 300 to 325 us (5.2 to 5.6).
 // Bound by HBM, for small layers (H 2048, I 768: 10 us a token) by the ends.  Three
-// steps in flight: 1 to 2 us slower for one token, no faster for sixteen.
+// steps in flight: 1 to 2 us slower for one token, no faster for sixteen.  Every copy
+// of a step's code comes cold at each launch: with two steps' loads in front of the
+// loop in place of one the small layer's kernels took 1 us more each (FP8, 4 tokens:
+// 24.8 and 15.8 us, now 24.0 and 14.5).
 
 template <bool FP8, int NG>
 __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
@@ -615,22 +620,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
 
   at.i = blockIdx.x;
   set_tile();
-  Step x[kDepth];
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) issue(x[d]);
+  Step x[2];
+  issue(x[0]);
   int unit = blockIdx.x, s = 0;
-  start(unit);
   for (;;) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
+    for (int d = 0; d < 2; ++d) {
+      issue(x[d ^ 1]);
+      if (s == 0) start(unit);
       add(x[d]);
-      issue(x[d]);
       if (++s == steps) {
         finish(unit);
         unit += stride;
         if (unit >= units) return;
         s = 0;
-        start(unit);
       }
     }
   }
@@ -807,9 +810,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
 
   at.i = blockIdx.x;
   set_tile();
-  Step x[kDepth];
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) issue(x[d]);
+  Step x[2];
+  issue(x[0]);
   clear();
   if (steps == 0) {                                      // no token has an expert
     for (int i = blockIdx.x; i < tiles; i += stride) finish(i);
@@ -818,9 +820,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
   int i = blockIdx.x, s = 0;
   for (;;) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
+    for (int d = 0; d < 2; ++d) {
+      issue(x[d ^ 1]);
       add(x[d]);
-      issue(x[d]);
       if (++s == steps) {
         finish(i);
         i += stride;
