@@ -8,6 +8,7 @@ library is missing or the device is not a gfx950 the call raises.
 """
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -570,6 +571,17 @@ def _out(t, shape, dtype, like, name="out"):
     return _is(t, dtype, name, shape)
 
 
+def _out_like(t, x, name="out"):
+    """_out of x's own shape and type; x is contiguous."""
+    return torch.empty_like(x) if t is None else _is(t, x.dtype, name, x.shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, *sizes):
+    """Workspace size of the entry point that `name` sizes: of the sizes alone."""
+    return getattr(lib(), name)(*sizes)
+
+
 def _scale_blocks(n):
     return (n + 127) // 128
 
@@ -768,16 +780,20 @@ def _rmsnorm(x, w, residual, eps, y, q, sf, h, rstd, need_y, need_q, need_rstd):
     shape = x.shape
     T, H = shape
     wide = _norm_weight(w, H)
+    dense = x.is_contiguous()
     r, ld_r = None, 0
     if residual is not None:
         _rows_of(residual, "residual")
         if residual.shape != shape:
             raise ValueError(f"residual must have shape {(T, H)} (got {tuple(residual.shape)})")
-        h = _out(h, shape, torch.bfloat16, x, "h")
+        h = _out_like(h, x, "h") if dense else _out(h, shape, torch.bfloat16, x, "h")
         r, ld_r = residual.data_ptr(), _ld(residual)
     elif h is not None:
         raise ValueError("h is x without a residual: no tensor to write it to")
-    y = _out(y, shape, torch.bfloat16, x, "y") if need_y else None
+    if not need_y:
+        y = None
+    else:
+        y = _out_like(y, x, "y") if dense else _out(y, shape, torch.bfloat16, x, "y")
     if need_q:
         q = _out(q, shape, FP8, x, "q")
         sf = _out(sf, (T, _scale_blocks(H)), torch.float32, x, "sf")
@@ -826,13 +842,13 @@ def rmsnorm_bwd(dy, h, w, rstd, dh=None, need_dw=True, out=None, workspace=None)
     if dh is not None:
         _is(dh, torch.bfloat16, "dh", (T, H))
     dx, dw = out if out is not None else (None, None)
-    dx = _out(dx, (T, H), torch.bfloat16, dy, "dx")
+    dx = _out_like(dx, dy, "dx")
     ws = None
     n = 0
     if need_dw:
         dw = _out(dw, (H,), torch.float32, dy, "dw")
         if workspace is None:
-            n = lib().nvfp4_rmsnorm_bwd_workspace_size(T, H)
+            n = _workspace_bytes("nvfp4_rmsnorm_bwd_workspace_size", T, H)
             ws = dy.new_empty(n, dtype=torch.uint8)
         else:
             ws = _is(workspace, torch.uint8, "workspace")
@@ -853,9 +869,9 @@ def _few(name, x, topk_ids, topk_w, H, I, E, weights, out, workspace):
         raise ValueError("weight shapes do not match x")
     _is(topk_ids, torch.int32, "topk_ids", (T, k))
     _is(topk_w, torch.float32, "topk_w", (T, k))
-    o = _out(out, (T, H), torch.bfloat16, x)
+    o = _out_like(out, x)
     if workspace is None:
-        n = lib().moe_expert_forward_few_workspace_size(T, I, k)
+        n = _workspace_bytes("moe_expert_forward_few_workspace_size", T, I, k)
         ws = x.new_empty(n, dtype=torch.uint8)
     else:
         ws = _is(workspace, torch.uint8, "workspace")
