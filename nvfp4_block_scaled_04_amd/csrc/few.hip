@@ -396,7 +396,7 @@ __device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
 // steps in flight: 1 to 2 us slower for one token, no faster for sixteen.  Every copy
 // of a step's code comes cold at each launch: with two steps' loads in front of the
 // loop in place of one the small layer's kernels took 1 us more each (FP8, 4 tokens:
-// 24.8 and 15.8 us, now 24.0 and 14.5).
+// 24.8 and 15.8 us, now 23.8 and 14.4).
 
 template <bool FP8, int NG>
 __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
@@ -646,9 +646,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
 // wave's own sums in LDS, [token][quarter][column], so a token gets nothing from
 // experts it did not choose, whatever these hold.
 //
-// Measured as above: one token FP8 22 us (117 MB), NVFP4 18 us (66 MB); sixteen FP8 223
-// to 240 us (6.2 to 6.7 TB/s), NVFP4 150 to 172 us (4.9 to 5.6); H 2048, I 768: one
-// token 5 us.
+// Measured as above: one token FP8 21 us (117 MB), NVFP4 18 us (66 MB); sixteen FP8 223
+// to 240 us (6.2 to 6.7 TB/s), NVFP4 150 to 175 us (4.8 to 5.6).  Bound by HBM; H 2048,
+// I 768, one token and four NVFP4 experts, 5 us: by the ends.
 
 template <bool FP8, int RF, int NG>
 __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
