@@ -25,6 +25,7 @@
 // lane and row group.
 //
 // Equal inputs give equal bits: waves and quarters are joined in a fixed order.
+#include <climits>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -265,10 +266,8 @@ struct Format {
 struct FewParams {
   FewArgs a;
   Weights w;                    // w1 (up) or w2 (down)
-  int split;                    // up: log2 of the waves a tile
   int tiles;                    // up: of one entry; down: all
-  float inv_tiles;              // up: 1 / tiles
-  int steps;                    // up: K steps a wave
+  float inv_tiles, inv_grid;    // up: 1 / tiles, 1 / workgroups
   int64_t t_bytes;              // of x or of one plane of h
 };
 
@@ -430,9 +429,24 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
   if (p.T * p.k <= 64) build_small(p, kTok, L, S.build);
   else build_large(p, kTok, L, S.build);
 
-  const int split = 1 << P.split, subs = kWaves >> P.split, sub = wave >> P.split, part = wave & (split - 1);
   const int I = W.N / 2, per = P.tiles, tiles = __builtin_amdgcn_readfirstlane(L.n) * per;
-  const int units = (tiles + subs - 1) >> (3 - P.split), stride = gridDim.x, steps = P.steps;
+  // Waves a tile (their log2, sp): the fewest rounds of K steps, where the join of
+  // several costs two fifths of a step a round.  1, 2, 4, 8 waves, us: FP8 one token
+  // 57, 38, 38, 41, small layer of four tokens 24, 25, 22, 25; NVFP4 small 13, 11, 8,
+  // 8, its four tokens 16, 18, 18, 26, sixteen tokens 323, 303, 310, 314.
+  int sp = 0, best = INT_MAX;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = ((tiles << i) + kWaves - 1) / kWaves;
+    const int rounds = __builtin_amdgcn_readfirstlane((int)((float)(n - 1) * P.inv_grid)) + 1;
+    const int cost = rounds * (5 * ((W.KS + (1 << i) - 1) >> i) + (i > 0 ? 2 : 0));
+    if (cost < best) {
+      best = cost;
+      sp = i;
+    }
+  }
+  const int split = 1 << sp, subs = kWaves >> sp, sub = wave >> sp, part = wave & (split - 1);
+  const int units = (tiles + subs - 1) >> (3 - sp), stride = gridDim.x, steps = (W.KS + split - 1) >> sp;
   if ((int)blockIdx.x >= units) return;
   const auto rx = rsrc_of(p.x, P.t_bytes);
   const int lane_col = kCols / 4 * (r >> 2) + kCols / 16 * g;   // of this lane's tokens in a K step
@@ -857,17 +871,10 @@ hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
   p.tiles = (int)(a.I / 16);
   p.inv_tiles = 1.0f / (float)p.tiles;
   p.t_bytes = (int64_t)a.T * a.H * 2;
-  // Waves a tile of the first product: the fewest rounds of its K steps, the join
-  // of several waves counted as two steps, a wave's own end of a tile as one.
-  const int64_t tiles = live * p.tiles;
-  int64_t best = INT64_MAX;
-  for (int s = 3; s >= 0; --s) {
-    const int64_t c = up(up(tiles << s, kWaves), cus) * (up(p.w.KS, 1 << s) + (s > 0 ? 2 : 1));
-    if (c < best) { best = c; p.split = s; }
-  }
-  p.steps = (int)up(p.w.KS, 1 << p.split);
-  const int64_t units = up(tiles << p.split, kWaves);
-  few_up_kernel<FP8, NG><<<(unsigned)(units < cus ? units : cus), kThreads, 0, stream>>>(p);
+  const int64_t tiles = (live + pairs / (4 * NG)) * p.tiles;   // at most: entries are full but for one an expert
+  const int grid = (int)(tiles < cus ? tiles : cus);
+  p.inv_grid = 1.0f / (float)grid;
+  few_up_kernel<FP8, NG><<<grid, kThreads, 0, stream>>>(p);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   p.w = weights_of<FP8>(a.w2_q, a.w2_sf, a.H, a.I);
