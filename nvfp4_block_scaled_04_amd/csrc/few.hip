@@ -390,7 +390,7 @@ __device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
 // Measured, one MI355X, H 7168, I 2048, 8 of 256 experts a token: one token FP8 38
 // to 40 us (235 MB), NVFP4 28 to 30 us (132 MB), of which 2.6 us are an empty
 // launch, 1 the list, 3 the way to the first weights and 2 the end; sixteen tokens
-// (102 experts) FP8 455 to 490 us (6.1 to 6.5 TB/s), NVFP4 300 to 325 us (5.2 to 5.6).
+// (102 experts) FP8 464 us (6.5 TB/s), NVFP4 305 us (5.5).
 // Bound by HBM, for small layers (H 2048, I 768: 10 us a token) by the ends.  Three
 // steps in flight: 1 to 2 us slower for one token, no faster for sixteen.  Every copy
 // of a step's code comes cold at each launch: with two steps' loads in front of the
