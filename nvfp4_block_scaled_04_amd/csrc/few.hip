@@ -885,7 +885,8 @@ hipError_t launch(const FewArgs& a, int cus, hipStream_t stream) {
     few_down_kernel<FP8, RF, NG><<<p.tiles < cus ? p.tiles : cus, kThreads, 0, stream>>>(p);
   };
   // Columns a tile: those that make about one tile a CU (7168: 28 columns, one token
-  // FP8 22 us, 32 columns 26, 16 columns in two rounds 28), eight at least.
+  // FP8 22 us, 32 columns 26, 16 columns in two rounds 28; 2048: 8 columns, four tokens,
+  // 14.5 us, 16 columns 17.9), eight at least.
   if (a.H <= 8 * cus) down(std::integral_constant<int, 2>{});
   else if (a.H <= 16 * cus) down(std::integral_constant<int, 4>{});
   else if (a.H <= 28 * cus) down(std::integral_constant<int, 7>{});
@@ -899,9 +900,10 @@ hipError_t launch_few(const FewArgs& a, hipStream_t stream) {
   int cus = 0;
   const hipError_t err = device_cus(cus);
   if (err != hipSuccess) return err;
-  // Entries of eight tokens, two groups an instruction's weights, from three tokens an
-  // expert on average (7168, 2048, 32 FP8 experts: four tokens each 286 us, in entries
-  // of four 338; two each 239, in entries of four 236).
+  // Entries of eight tokens, two groups an instruction's weights, from more than two
+  // tokens an expert on average (7168, 2048, 32 experts, both products: four tokens each
+  // FP8 257 us and NVFP4 184, in entries of four 311 and 212; three each FP8 244, in fours
+  // 261; two each 215 and 150, in fours 211 and 144).
   const bool busy = a.T > 4 && (int64_t)a.T * a.k > 2 * (int64_t)a.E;
   if (a.fp8) return busy ? launch<true, 2>(a, cus, stream) : launch<true, 1>(a, cus, stream);
   return busy ? launch<false, 2>(a, cus, stream) : launch<false, 1>(a, cus, stream);
