@@ -575,7 +575,7 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const v
  *   [gate | up] = W1[e] x[t],   h = silu(gate) * up   (fp32),
  *   out[t] = bf16_rne( sum_j topk_w[t][j] * W2[e] h ),
  * products and sums in fp32, each h rounded to 11 bits of significand or more (and
- * to 2^-39 of the largest of 128).  With NVFP4 weights what lies below 2^-29 of the
+ * to 2^-38 of the largest of 128).  With NVFP4 weights what lies below 2^-29 of the
  * token's largest |x| is lost, and a token that holds an infinity or NaN gives NaN.
  * Ids outside [0, E) contribute nothing (a token with none but these gives zeros);
  * an id may come twice in a row.  A shared expert is a further expert and a

@@ -761,15 +761,21 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
         int top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max((int)(lo >> (8 * i) & 255), (int)(hi >> (8 * i) & 255)));
-        const _Float16 p0 = __builtin_ldexpf16((_Float16)1.0f, (int)(own & 255) - top), p1 = __builtin_ldexpf16((_Float16)1.0f, (int)(own >> 8 & 255) - top);
-        const half2v f0{p0, p0}, f1{p1, p1};
+        auto shift = [&](int d0, int d1) {
+          const _Float16 p0 = __builtin_ldexpf16((_Float16)1.0f, d0), p1 = __builtin_ldexpf16((_Float16)1.0f, d1);
+          const half2v f0{p0, p0}, f1{p1, p1};
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+          for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int two = x.t[j][0][m][i];
-            x.t[j][0][m][i] = __builtin_bit_cast(int, __builtin_bit_cast(half2v, two) * (m < 2 ? f0 : f1));
-          }
+            for (int i = 0; i < 4; ++i) {
+              const int two = x.t[j][0][m][i];
+              x.t[j][0][m][i] = __builtin_bit_cast(int, __builtin_bit_cast(half2v, two) * (m < 2 ? f0 : f1));
+            }
+        };
+        // FP16's least power of two is 2^-24: what lies further below takes two factors
+        const int d0 = (int)(own & 255) - top, d1 = (int)(own >> 8 & 255) - top;
+        shift(max(d0, -24), max(d1, -24));
+        if (__any(min(d0, d1) < -24)) shift(min(d0 + 24, 0), min(d1 + 24, 0));
         back[j] = ldexpf(1.0f, top - 141);
       }
     }
