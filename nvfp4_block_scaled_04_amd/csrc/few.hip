@@ -26,6 +26,7 @@
 //
 // Equal inputs give equal bits: waves and quarters are joined in a fixed order.
 #include <climits>
+#include <cstddef>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -72,17 +73,19 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // The live experts in order of their first pair, each cut into entries of at
 // most `cap` tokens.  A row of h is one (expert, token); rows follow the entries.
-struct Entry {
+struct alignas(16) Entry {      // the second product reads one as a uint4
   uint16_t e, row;              // expert, first row
   uint32_t count;               // rows
   uint8_t tok[8];               // their tokens
 };
 
 struct Live {
-  int n;                        // entries
   Entry entry[kPairs];
   float coef[kPairs];           // a row's weight
+  int n;                        // entries
 };
+static_assert(sizeof(Entry) == 16 && alignof(Entry) >= alignof(uint4) && offsetof(Live, entry) % 16 == 0,
+              "an entry is read as a uint4");
 
 struct LiveScratch {
   int first[kMaxExperts];       // first pair of an expert, then its place among the experts
