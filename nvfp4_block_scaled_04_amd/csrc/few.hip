@@ -69,6 +69,15 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Between LDS writes of the wave's lanes and reads of theirs by others, or the
+// other way round.  The hardware keeps a wave's LDS accesses in order; this keeps the
+// compiler from moving them past each other, and costs no instruction.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ------------------------------------------------------------ the work
 //
 // The live experts in order of their first pair, each cut into entries of at
@@ -133,14 +142,14 @@ __device__ __forceinline__ void build_small(const FewArgs& p, int cap, Live& L, 
     first_of[lane] = 64;
     count_of[lane] = 0;
     if (on) S.first[e] = lane;
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
     int mask = 0, first = 64, count = 0, by = 0;
     if (on) {
       by = S.first[e];
       atomicOr(&mask_of[by], 1 << t);
       atomicMin(&first_of[by], lane);
       atomicAdd(&count_of[by], 1);
-      __builtin_amdgcn_wave_barrier();
+      wave_order();
       mask = mask_of[by];
       first = first_of[by];
       count = count_of[by];
@@ -540,7 +549,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
       s0 = g < 2 ? x.w.sc[0][0] : x.w.sc[0][1];
       s1 = g < 2 ? x.w.sc[1][0] : x.w.sc[1][1];
     } else {
+      wave_order();                                      // the last step's scales are read
       *reinterpret_cast<int4v*>(&scales[wave].v[g][2 * r][0]) = x.w.s;
+      wave_order();
 #pragma unroll
       for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -576,6 +587,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
   // the unit's sums over its waves and quarters, SwiGLU, and h in its 16 bits
   auto finish = [&](int unit) {
     if (split > 1) lds_barrier();                        // the last unit's sums are read
+    else wave_order();
     if ((r >> 2) == g) {
 #pragma unroll
       for (int j = 0; j < NG; ++j)
@@ -587,7 +599,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
 #pragma unroll
       for (int f = 0; f < RF; ++f) acc[j][f] = float4v{0, 0, 0, 0};
     if (split > 1) lds_barrier();
-    else __builtin_amdgcn_wave_barrier();
+    else wave_order();
     // a thread an output: 16 columns of four tokens a wave, as many waves as tiles
     if (wave >= subs) return;
     const int c = lane & 15, t = lane >> 4, tile = unit * subs + wave;
@@ -752,11 +764,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewParams P) {
   };
   auto add = [&](Step& x) {
     float s0, s1, back[NG];
+    wave_order();                                        // the last step's sums are written, by other lanes of a token, and its scales read
     if constexpr (FP8) {
       s0 = g < 2 ? x.w.sc[0][0] : x.w.sc[0][1];
       s1 = g < 2 ? x.w.sc[1][0] : x.w.sc[1][1];
     } else {
       *reinterpret_cast<int4v*>(&scales[wave].v[g][2 * r][0]) = x.w.s;
+      wave_order();
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         // this quarter's columns to one power of two: its largest
