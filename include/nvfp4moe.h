@@ -554,8 +554,9 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* a_q, const float* a_sf, int64
  *   dx = bf16_rne( dh + rstd * (g - n * mean of g*n) ), the gradient of x and of
  *        residual alike;
  *   dw = sum over rows of dy * n  (fp32, nullable).
- * dy, dh, h, dx BF16 [rows][cols], contiguous; dw float [cols], zero for no
- * rows.  dx may be dy or dh itself.  Every sum has a fixed order: equal inputs
+ * dy, dh, h, dx BF16 [rows][cols], contiguous (nvfp4_rmsnorm_bwd_ld: rows of h
+ * ld_h >= cols elements apart, a multiple of 8, as x may be where h is x); dw float
+ * [cols], zero for no rows.  dx may be dy or dh itself.  Every sum has a fixed order: equal inputs
  * give equal bits.
  * Workspace: with dw nvfp4_rmsnorm_bwd_workspace_size() bytes, 16-byte aligned.
  * Outputs must not overlap inputs otherwise, nor each other.
@@ -567,6 +568,9 @@ size_t nvfp4_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols);
 nvfp4_status nvfp4_rmsnorm_bwd(const void* dy_bf16, const void* dh_bf16, const void* h_bf16,
                                const float* rstd, const void* w, int w_fp32, int64_t rows, int64_t cols,
                                void* dx_bf16, float* dw, void* ws, size_t ws_bytes, void* stream);
+nvfp4_status nvfp4_rmsnorm_bwd_ld(const void* dy_bf16, const void* dh_bf16, const void* h_bf16, int64_t ld_h,
+                                  const float* rstd, const void* w, int w_fp32, int64_t rows, int64_t cols,
+                                  void* dx_bf16, float* dw, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * The expert layer for a few tokens, in two kernels.

@@ -77,6 +77,8 @@ SIGNATURES = {
     "nvfp4_rmsnorm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
     "nvfp4_rmsnorm_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int64,
                                   c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "nvfp4_rmsnorm_bwd_ld": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int,
+                                     c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_expert_forward_few_workspace_size": (c_size_t, [c_int64, c_int64, c_int]),
     "moe_expert_forward_few": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_int, c_int, c_void_p,
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
@@ -828,15 +830,17 @@ def fp8_rmsnorm(x, w, residual=None, eps=1e-6, need_y=False, need_rstd=False, ou
 
 def rmsnorm_bwd(dy, h, w, rstd, dh=None, need_dw=True, out=None, workspace=None):
     """Gradient of rmsnorm and fp8_rmsnorm: dy (T, H) bf16 the gradient of the
-    normalised rows, h and rstd as they returned them, dh (T, H) bf16 the gradient
-    that reaches h from elsewhere -> (dx (T, H) bf16, of x and residual alike,
-    dw (H,) float32 or None).  out: (dx, dw) tensors to write; dx may be dy or dh.
+    normalised rows, h (rows may be spaced apart) and rstd as they returned them,
+    dh (T, H) bf16 the gradient that reaches h from elsewhere -> (dx (T, H) bf16, of
+    x and residual alike, dw (H,) float32 or None).  out: (dx, dw) tensors to write; dx may be dy or dh.
     workspace: uint8 tensor of nvfp4_rmsnorm_bwd_workspace_size(T, H) bytes."""
     _is(dy, torch.bfloat16, "dy")
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D")
     T, H = dy.shape
-    _is(h, torch.bfloat16, "h", (T, H))
+    _rows_of(h, "h")
+    if h.shape != dy.shape:
+        raise ValueError(f"h must have shape {(T, H)} (got {tuple(h.shape)})")
     wide = _norm_weight(w, H)
     _is(rstd, torch.float32, "rstd", (T,))
     if dh is not None:
@@ -855,8 +859,8 @@ def rmsnorm_bwd(dy, h, w, rstd, dh=None, need_dw=True, out=None, workspace=None)
             n = ws.numel()
     else:
         dw = None
-    _call("nvfp4_rmsnorm_bwd", (dy, dh, h, rstd, w, dx, dw, ws), dy.data_ptr(), _ptr(dh), h.data_ptr(),
-          rstd.data_ptr(), w.data_ptr(), wide, T, H, dx.data_ptr(), _ptr(dw), _ptr(ws), n)
+    _call("nvfp4_rmsnorm_bwd_ld", (dy, dh, h, rstd, w, dx, dw, ws), dy.data_ptr(), _ptr(dh), h.data_ptr(),
+          _ld(h), rstd.data_ptr(), w.data_ptr(), wide, T, H, dx.data_ptr(), _ptr(dw), _ptr(ws), n)
     return dx, dw
 
 

@@ -981,13 +981,16 @@ size_t nvfp4_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols) {
   return sizeof(float) * (size_t)nvfp4::rmsnorm_bwd_groups(rows, cols) * (size_t)cols;
 }
 
-nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const float* rstd, const void* w,
-                               int w_fp32, int64_t rows, int64_t cols, void* dx, float* dw, void* ws,
-                               size_t ws_bytes, void* stream) {
+nvfp4_status nvfp4_rmsnorm_bwd_ld(const void* dy, const void* dh, const void* h, int64_t ld_h, const float* rstd,
+                                  const void* w, int w_fp32, int64_t rows, int64_t cols, void* dx, float* dw,
+                                  void* ws, size_t ws_bytes, void* stream) {
   nvfp4_status st = check_norm(rows, cols, 1.0f);
   if (st != NVFP4_OK) return st;
   if (w_fp32 != 0 && w_fp32 != 1) return fail(NVFP4_ERR_INVALID_ARG, "w_fp32 must be 0 or 1 (got %d)", w_fp32);
+  if (ld_h < cols || ld_h % 8 || ld_h >= (int64_t(1) << 40))
+    return fail(NVFP4_ERR_SHAPE, "ld_h must be >= cols and a multiple of 8");
   if (rows == 0 && !dw) return NVFP4_OK;
+  if (rows > 0 && ld_h >= (int64_t(1) << 60) / rows) return fail(NVFP4_ERR_SHAPE, "rows * ld_h must be below 2^60");
   if (!w || (rows > 0 && (!dy || !h || !rstd || !dx)))
     return fail(NVFP4_ERR_INVALID_ARG, "dy, h, rstd, w and dx must be non-NULL");
   if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
@@ -996,10 +999,10 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, co
   const size_t need = dw ? nvfp4_rmsnorm_bwd_workspace_size(rows, cols) : 0;
   if (dw && (!ws || ws_bytes < need || !aligned(ws, 16)))
     return fail(NVFP4_ERR_WORKSPACE, "nvfp4_rmsnorm_bwd needs %zu workspace bytes, 16-byte aligned (got %zu)", need, ws_bytes);
-  const int64_t n = 2 * rows * cols;
+  const int64_t n = 2 * rows * cols, hb = 2 * ((rows - 1) * ld_h + cols);
   // dx may be dy or dh, rows in their places
   const Span outs[] = {{dx, n}, {dw, 4 * cols}, {dw ? ws : nullptr, (int64_t)need}};
-  const Span ins[] = {{dy == dx ? nullptr : dy, n}, {dh == dx ? nullptr : dh, n}, {h, n}, {rstd, 4 * rows},
+  const Span ins[] = {{dy == dx ? nullptr : dy, n}, {dh == dx ? nullptr : dh, n}, {h, hb}, {rstd, 4 * rows},
                       {w, (w_fp32 ? 4 : 2) * cols}};
   if (rows > 0 && any_overlap(outs, ins))
     return fail(NVFP4_ERR_INVALID_ARG, "outputs and workspace must not overlap the inputs (but dx may be dy or dh) or each other");
@@ -1011,11 +1014,18 @@ nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, co
   a.dy = static_cast<const uint16_t*>(dy);
   a.dh = static_cast<const uint16_t*>(dh);
   a.h = static_cast<const uint16_t*>(h);
+  a.ld_h = ld_h;
   a.rstd = rstd; a.w = w; a.wide = w_fp32 != 0; a.rows = rows; a.cols = (int)cols;
   a.dx = static_cast<uint16_t*>(dx);
   a.part = dw ? static_cast<float*>(ws) : nullptr;
   a.dw = dw;
   return finish(nvfp4::launch_rmsnorm_bwd(a, static_cast<hipStream_t>(stream)), "nvfp4_rmsnorm_bwd launch");
+}
+
+nvfp4_status nvfp4_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const float* rstd, const void* w,
+                               int w_fp32, int64_t rows, int64_t cols, void* dx, float* dw, void* ws,
+                               size_t ws_bytes, void* stream) {
+  return nvfp4_rmsnorm_bwd_ld(dy, dh, h, cols, rstd, w, w_fp32, rows, cols, dx, dw, ws, ws_bytes, stream);
 }
 
 size_t moe_expert_forward_few_workspace_size(int64_t T, int64_t I, int k) {

@@ -170,6 +170,7 @@ hipError_t launch_rmsnorm(const RmsnormArgs& a, hipStream_t stream);
 
 struct RmsnormBwdArgs {
   const uint16_t *dy, *dh, *h;   // dh nullable
+  int64_t ld_h;                  // rows of h this far apart
   const float* rstd;
   const void* w;
   bool wide;

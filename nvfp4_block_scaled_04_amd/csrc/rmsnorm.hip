@@ -206,7 +206,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void rmsnorm_bwd_kern
       const int vec = i * LANES + lane;
       x.h[i] = x.dy[i] = x.dh[i] = make_uint4(0, 0, 0, 0);
       if (on && vec < vecs) {
-        x.h[i] = load16<STREAM>(p.h + row * p.cols + 8 * vec);
+        x.h[i] = load16<STREAM>(p.h + row * p.ld_h + 8 * vec);
         x.dy[i] = load16<STREAM>(p.dy + row * p.cols + 8 * vec);
         if (p.dh) x.dh[i] = load16<STREAM>(p.dh + row * p.cols + 8 * vec);
       }
