@@ -869,6 +869,7 @@ def _few(name, x, topk_ids, topk_w, H, I, E, weights, out, workspace):
     if x.dim() != 2 or not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
         raise ValueError("x and topk_ids must be 2-D")
     T, k = x.shape[0], topk_ids.shape[1]
+    _int32(k, "k")
     if x.shape[1] != H:
         raise ValueError("weight shapes do not match x")
     _is(topk_ids, torch.int32, "topk_ids", (T, k))
@@ -887,6 +888,7 @@ def _few(name, x, topk_ids, topk_w, H, I, E, weights, out, workspace):
 
 def few_workspace(T, I, k, device):
     """Workspace of the two calls below."""
+    _int32(k, "k")
     return _workspace(lib().moe_expert_forward_few_workspace_size(T, I, k), device)
 
 
