@@ -869,15 +869,17 @@ struct Span {
   int64_t n;
 };
 
-// does any output (nullptr: absent) overlap an input or another output?
+// does any output (nullptr or no bytes: absent) overlap an input or another output?
 template <size_t N, size_t M>
 bool any_overlap(const Span (&out)[N], const Span (&in)[M]) {
+  auto meet = [](const Span& a, const Span& b) {
+    return a.p && b.p && a.n > 0 && b.n > 0 && overlap(a.p, a.n, b.p, b.n);
+  };
   for (size_t i = 0; i < N; ++i) {
-    if (!out[i].p) continue;
     for (size_t j = 0; j < M; ++j)
-      if (in[j].p && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+      if (meet(out[i], in[j])) return true;
     for (size_t j = i + 1; j < N; ++j)
-      if (out[j].p && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+      if (meet(out[i], out[j])) return true;
   }
   return false;
 }
@@ -999,15 +1001,13 @@ nvfp4_status nvfp4_rmsnorm_bwd_ld(const void* dy, const void* dh, const void* h,
   const size_t need = dw ? nvfp4_rmsnorm_bwd_workspace_size(rows, cols) : 0;
   if (dw && (!ws || ws_bytes < need || !aligned(ws, 16)))
     return fail(NVFP4_ERR_WORKSPACE, "nvfp4_rmsnorm_bwd needs %zu workspace bytes, 16-byte aligned (got %zu)", need, ws_bytes);
-  const int64_t n = 2 * rows * cols, hb = 2 * ((rows - 1) * ld_h + cols);
+  const int64_t n = 2 * rows * cols, hb = rows > 0 ? 2 * ((rows - 1) * ld_h + cols) : 0;
   // dx may be dy or dh, rows in their places
   const Span outs[] = {{dx, n}, {dw, 4 * cols}, {dw ? ws : nullptr, (int64_t)need}};
   const Span ins[] = {{dy == dx ? nullptr : dy, n}, {dh == dx ? nullptr : dh, n}, {h, hb}, {rstd, 4 * rows},
                       {w, (w_fp32 ? 4 : 2) * cols}};
-  if (rows > 0 && any_overlap(outs, ins))
+  if (any_overlap(outs, ins))
     return fail(NVFP4_ERR_INVALID_ARG, "outputs and workspace must not overlap the inputs (but dx may be dy or dh) or each other");
-  if (rows > 0 && ((dy == dx && dw && overlap(dw, 4 * cols, dy, n)) || (dh && dh == dx && dw && overlap(dw, 4 * cols, dh, n))))
-    return fail(NVFP4_ERR_INVALID_ARG, "dw must not overlap the inputs");
   st = check_arch();
   if (st != NVFP4_OK) return st;
   nvfp4::RmsnormBwdArgs a{};

@@ -38,3 +38,14 @@ def test_rmsnorm_bwd_ld_rejects(L, kw, status):
 
 def test_rmsnorm_bwd_ld_of_no_rows(L):
     assert L.nvfp4_rmsnorm_bwd_ld(*_bwd(rows=0, dw=None, dy=None, h=None, w=None, rstd=None, dx=None, ws=None)) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(dw=P[4]), dict(dw=P[4] + 128), dict(ws=P[4]), dict(dw=P[7] + 16)])
+def test_rmsnorm_bwd_of_no_rows_keeps_its_weight(L, kw):
+    """dw of no rows is written, so it may not lie over w or the workspace either."""
+    a = dict(rows=0, dy=None, dh=None, h=None, rstd=None, dx=None)
+    a.update(kw)
+    assert L.nvfp4_rmsnorm_bwd_ld(*_bwd(**a)) == -1
+    a["ld_h"] = 64
+    b = _bwd(**a)
+    assert L.nvfp4_rmsnorm_bwd(*b[:3], *b[4:]) == -1
