@@ -859,7 +859,7 @@ nvfp4_status check_norm(int64_t rows, int64_t cols, float eps) {
   if (cols < 8 || cols % 8 || cols > kNormMaxCols)
     return fail(NVFP4_ERR_SHAPE, "cols must be a positive multiple of 8 up to %lld (got %lld)",
                 (long long)kNormMaxCols, (long long)cols);
-  if (!(eps >= 1.0e-30f) || eps > 3.0e38f)               // below, squares that count would be subnormal
+  if (!(eps >= 1.0e-30f) || eps > 3.0e38f)               // down to here the scaled sums of squares are exact enough
     return fail(NVFP4_ERR_INVALID_ARG, "eps must be finite and at least 1e-30");
   return NVFP4_OK;
 }

@@ -90,8 +90,10 @@ struct W8 {
 };
 
 // Squares are summed times 2^-16 (at most 2^15 columns), so that the sum stays
-// finite wherever the mean does.  What this makes subnormal lies below 2^-24 of
-// the smallest eps that is allowed, 1e-30.
+// finite wherever the mean does.  Sums that this makes subnormal (a mean below 2^-113
+// in rows of 128, where the smallest eps allowed, 1e-30, is 2^-99.7) need fp32's
+// subnormal numbers, which this build keeps: their roundings of 2^-150 are 2^-134
+// each in the mean, 2^-34 of that eps; flushed to zero they would cost 2^-14 of 1/rms.
 constexpr float kSquareScale = 1.52587890625e-05f;
 
 // LANES lanes a row, NV vectors of eight columns each (vector i * LANES + lane): the
