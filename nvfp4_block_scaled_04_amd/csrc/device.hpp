@@ -121,4 +121,12 @@ __device__ __forceinline__ void quantize_block16(const float (&x)[16], float gs,
                   x[15] * r);
 }
 
+// Workgroup barrier for what went through LDS, without a fence: global loads in
+// flight stay there.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace nvfp4

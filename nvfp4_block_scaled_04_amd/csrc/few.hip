@@ -62,13 +62,6 @@ __device__ __forceinline__ float uniform_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)p;
 }
 
-// barrier without a fence: the loads in flight stay there
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Between LDS writes of the wave's lanes and reads of theirs by others, or the
 // other way round.  The hardware keeps a wave's LDS accesses in order; this keeps the
 // compiler from moving them past each other, and costs no instruction.

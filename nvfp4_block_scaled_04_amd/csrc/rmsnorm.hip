@@ -40,13 +40,6 @@ __device__ __forceinline__ void store8(uint8_t* p, const uint2& v) {
   else *reinterpret_cast<uint2*>(p) = v;
 }
 
-// barrier without a fence: the loads in flight stay there
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Sum of v over the LANES lanes of a row; every lane gets it.  red: LDS of
 // threads / 64 floats, free for the next sum only after a barrier.
 template <int LANES>
