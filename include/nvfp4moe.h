@@ -583,7 +583,8 @@ nvfp4_status nvfp4_rmsnorm_bwd_ld(const void* dy_bf16, const void* dh_bf16, cons
  * token's largest |x| is lost, and a token that holds an infinity or NaN gives NaN.
  * Ids outside [0, E) contribute nothing (a token with none but these gives zeros);
  * an id may come twice in a row.  A shared expert is a further expert and a
- * further slot of weight 1.  Each live expert's weights are read once.
+ * further slot of weight 1.  A live expert's weights are read once for every four
+ * of its tokens, for every eight where T > 4 and T*k > 2*E.
  * x, out BF16 [T][H]; topk_ids int32, topk_w float [T][k].
  * moe_expert_forward_few: the weights of moe_expert_forward (w1 interleaved,
  *   packed by nvfp4_pack_weights; E2M1 * E4M3 / gs).

@@ -5,7 +5,8 @@
 //   down:  out[t][n] = bf16( sum over experts e of W2[e][n] . h_te )
 // Weights FP8 (one scale per 128 x 128) or packed NVFP4 (E4M3 per 16, a global
 // scale an expert).  Activations are not quantised: the bytes of each live
-// expert's weights, read once, are the bound.
+// expert's weights are the bound.  They are read once for every four of its
+// tokens, or every eight (launch_few): once in all where routing is even.
 //
 // FP8 weights enter the matrix unit as BF16 (exact), with x as it is and h as two
 // BF16, its rounding and what that leaves (16 bits in all).  NVFP4 weights enter
@@ -293,7 +294,7 @@ __device__ __forceinline__ int group_at(const Weights& W, int row) {
 }
 
 // Loads of K step b of the row groups at `at` of expert e; none if !on.  Past the
-// caches: each is read once.  block (FP8): the two 128-row blocks that the groups
+// caches: each is read once an entry.  block (FP8): the two 128-row blocks that the groups
 // lie in; scale_at (NVFP4): this lane's place in the scales of step 0.  TURN: the
 // groups are eight in a row, 256 bytes each, and load f takes group f ^ q of
 // quarter q: stages are 32 KiB apart, so one group's quarters would all come from
@@ -395,7 +396,7 @@ __device__ __forceinline__ uint32_t move_exponents(uint32_t v, uint32_t less) {
 // Measured, one MI355X, H 7168, I 2048, 8 of 256 experts a token: one token FP8 38
 // to 40 us (235 MB), NVFP4 28 to 30 us (132 MB), of which 2.6 us are an empty
 // launch, 1 the list, 3 the way to the first weights and 2 the end; sixteen tokens
-// (102 experts) FP8 464 us (6.5 TB/s), NVFP4 305 us (5.5).
+// (102 experts) FP8 442 to 464 us (6.5 to 6.8 TB/s), NVFP4 305 us (5.5).
 // Bound by HBM, for small layers (H 2048, I 768: 10 us a token) by the ends.  Three
 // steps in flight: 1 to 2 us slower for one token, no faster for sixteen.  Every copy
 // of a step's code comes cold at each launch: with two steps' loads in front of the
@@ -669,7 +670,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_up_kernel(FewParams P) {
 // experts it did not choose, whatever these hold.
 //
 // Measured as above: one token FP8 21 us (117 MB), NVFP4 18 us (66 MB); sixteen FP8 223
-// to 240 us (6.2 to 6.7 TB/s), NVFP4 150 to 175 us (4.8 to 5.6).  Bound by HBM; H 2048,
+// to 240 us (6.2 to 6.7 TB/s), NVFP4 164 to 175 us (4.8 to 5.1).  Bound by HBM; H 2048,
 // I 768, one token and four NVFP4 experts, 5 us: by the ends.
 
 template <bool FP8, int RF, int NG>
@@ -919,7 +920,9 @@ hipError_t launch_few(const FewArgs& a, hipStream_t stream) {
   // Entries of eight tokens, two groups an instruction's weights, from more than two
   // tokens an expert on average (7168, 2048, 32 experts, both products: four tokens each
   // FP8 257 us and NVFP4 184, in entries of four 311 and 212; three each FP8 244, in fours
-  // 261; two each 215 and 150, in fours 211 and 144).
+  // 261; two each 215 and 150, in fours 211 and 144).  All of that was routed evenly: an
+  // expert of many tokens among few pairs is read once for every four of them (one
+  // expert of sixteen tokens alone: FP8 38.6 us, 176 MB; 44 MB would be its weights once).
   const bool busy = a.T > 4 && (int64_t)a.T * a.k > 2 * (int64_t)a.E;
   if (a.fp8) return busy ? launch<true, 2>(a, cus, stream) : launch<true, 1>(a, cus, stream);
   return busy ? launch<false, 2>(a, cus, stream) : launch<false, 1>(a, cus, stream);
