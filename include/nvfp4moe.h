@@ -581,6 +581,8 @@ nvfp4_status nvfp4_rmsnorm_bwd_ld(const void* dy_bf16, const void* dh_bf16, cons
  * products and sums in fp32, each h rounded to 11 bits of significand or more (and
  * to 2^-38 of the largest of 128).  With NVFP4 weights what lies below 2^-29 of the
  * token's largest |x| is lost, and a token that holds an infinity or NaN gives NaN.
+ * With FP8 weights |x| and |topk_w h| have to stay below 2^112: codes times them are
+ * summed before their scale, which a larger one could take past fp32.
  * Ids outside [0, E) contribute nothing (a token with none but these gives zeros);
  * an id may come twice in a row.  A shared expert is a further expert and a
  * further slot of weight 1.  A live expert's weights are read once for every four

@@ -9,8 +9,9 @@
 // tokens, or every eight (launch_few): once in all where routing is even.
 //
 // FP8 weights enter the matrix unit as BF16 (exact), with x as it is and h as two
-// BF16, its rounding and what that leaves (16 bits in all).  NVFP4 weights enter
-// as FP16, in which a scale is one packed product for two weights (exact; in BF16
+// BF16, its rounding and what that leaves (16 bits in all).  A block's scale
+// multiplies the sums of 64 codes (448 at most) times these, which are finite where
+// they are below 2^112.  NVFP4 weights enter as FP16, in which a scale is one packed product for two weights (exact; in BF16
 // it would be three times the instructions, and decoding them bounds the kernels):
 // x with its exponents moved so that a token's largest just fits (exact down to
 // 2^-29 of that, below off by 2^-30 of it), h rounded to FP16 (11 bits, an eighth

@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
 @pytest.mark.parametrize("sx,s1,s2", [(1e20, 1e-20, 1e10), (1e-20, 1e20, 1e-10), (1e28, 1e-28, 1.0), (1e-28, 1e28, 1.0),
-                                      (1.0, 1.0, 1e-27), (1.0, 1.0, 1e28), (1e-12, 1.0, 1e24), (1e9, 1.0, 1e-25)])
+                                      (1.0, 1.0, 1e-27), (1.0, 1.0, 1e28), (1e-12, 1.0, 1e24), (1e9, 1.0, 1e-25),
+                                      (1e33, 1e-29, 1.0), (1.0, 2e16, 1e-28)])   # next to 2^112, FP8's limit of x and h
 def test_few_scales(monkeypatch, fmt, sx, s1, s2):
     rng = np.random.default_rng(17)
     T, H, I, E, k = 6, 384, 256, 4, 2
